@@ -18,7 +18,9 @@ BF16, F32 = 0, 1
 OUT_BF16, OUT_F32, OUT_F32_ACCUMULATE = 0, 1, 2
 ACT_SILU, ACT_RELU = 0, 1
 CAL_GLOBAL_ABS_ACT, CAL_PER_NEURON_PRED, CAL_PER_NEURON_RECALL = 0, 1, 2
+ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1
 MAX_BATCH = 16
+MAX_EXPERTS, MAX_TOPK = 512, 16
 
 
 class Layer(ctypes.Structure):
@@ -36,11 +38,26 @@ class Layer(ctypes.Structure):
     ]
 
 
+class MoELayer(ctypes.Structure):
+    """csffn_moe_layer."""
+
+    _fields_ = [
+        ("d", ctypes.c_int32),
+        ("h", ctypes.c_int32),
+        ("n_experts", ctypes.c_int32),
+        ("act", ctypes.c_int32),
+        ("w_gate", ctypes.c_void_p),
+        ("w_up", ctypes.c_void_p),
+        ("w_down_t", ctypes.c_void_p),
+    ]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _Z = ctypes.c_size_t
 _L = ctypes.POINTER(Layer)
+_M = ctypes.POINTER(MoELayer)
 
 SIGNATURES = {
     "csffn_version": (_I, []),
@@ -63,6 +80,14 @@ SIGNATURES = {
     "csffn_rmsnorm_bf16": (_I, [_P, _I, _I, _F, _P, _P]),
     "csffn_selftest_timeout": (_I, [_P, _Z, _I, _P]),
     "csffn_sparse_ffn_forward_static": (_I, [_L, _P, _I, _P, _P, _P, _P, _I, _P]),
+    "csffn_moe_logits": (_I, [_P, _P, _I, _I, _I, _P, _P]),
+    "csffn_moe_route": (_I, [_P, _I, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P]),
+    "csffn_moe_dispatch_workspace_size": (_Z, [_I, _I]),
+    "csffn_moe_dispatch": (_I, [_P, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _Z, _P]),
+    "csffn_moe_workspace_size": (_Z, [_M, _I]),
+    "csffn_moe_ffn_forward": (_I, [_M, _P, _P, _I, _P, _P, _Z, _P]),
+    "csffn_moe_combine": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _I, _P]),
+    "csffn_block_norm": (_I, [_P, _P, _I, _P, _P, _I, _P, _F, _F, _F, _I, _I, _P, _P, _I, _P]),
 }
 
 _lib = None

@@ -260,6 +260,193 @@ def selftest_timeout(ws: torch.Tensor, spin_limit: int, stream=None) -> None:
           "csffn_selftest_timeout")
 
 
+# ------------------------------------------------------------------------------ routed FFN, block norm
+
+class _Call:
+    """The tensors of one call: every one contiguous and on one CUDA device, which is made current for
+    the call (kernels launch on the current device), and the stream to launch on: the one given, or
+    that device's current one."""
+
+    __slots__ = ("index", "prev")
+
+    def __init__(self, first: torch.Tensor):
+        if not first.is_cuda:
+            raise ValueError("csffn takes CUDA tensors")
+        self.index = first.get_device()
+
+    def ptr(self, t: Optional[torch.Tensor], name: str, shape, *dtypes: torch.dtype):
+        if t is None:
+            return None
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError("csffn takes contiguous tensors")
+        if t.get_device() != self.index:
+            raise ValueError(f"{name} must be on the device of the call's other tensors (cuda:{self.index})")
+        return t.data_ptr()
+
+    def ws(self, ws: torch.Tensor):
+        return self.ptr(ws, "ws", ws.shape, torch.uint8)
+
+    def run(self, name: str, stream, *args) -> None:
+        s = stream.cuda_stream if stream is not None else torch.cuda.current_stream(self.index).cuda_stream
+        fn = getattr(load(), name)
+        if torch.cuda.current_device() == self.index:
+            status = fn(*args, s)
+        else:
+            with torch.cuda.device(self.index):
+                status = fn(*args, s)
+        if status != _abi.OK:
+            raise CsffnError(status, name)
+
+
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_CODE = {_BF16: _abi.BF16, _F32: _abi.F32}
+
+
+def _matrix(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, not {t.dim()}")
+    return t.shape
+
+
+@dataclass
+class MoELayer:
+    """Device copy of one routed FFN layer (bf16 [E, h, d] matrices) plus the csffn_moe_layer struct."""
+
+    w_gate: torch.Tensor
+    w_up: torch.Tensor
+    w_down_t: torch.Tensor
+    act: int
+    c: _abi.MoELayer = field(default=None, repr=False)
+
+    def __post_init__(self):
+        if self.w_gate.dim() != 3:
+            raise ValueError("w_gate must be [n_experts, h, d]")
+        call = _Call(self.w_gate)
+        E, h, d = self.w_gate.shape
+        ptrs = [call.ptr(w, n, self.w_gate.shape, _BF16)
+                for w, n in ((self.w_gate, "w_gate"), (self.w_up, "w_up"), (self.w_down_t, "w_down_t"))]
+        self.c = _abi.MoELayer(d, h, E, self.act, *ptrs)
+
+    @property
+    def d(self) -> int:
+        return self.c.d
+
+    @property
+    def h(self) -> int:
+        return self.c.h
+
+    @property
+    def n_experts(self) -> int:
+        return self.c.n_experts
+
+    def ref(self):
+        return ctypes.byref(self.c)
+
+
+def moe_workspace_size(layer: MoELayer, max_rows: int) -> int:
+    n = load().csffn_moe_workspace_size(layer.ref(), max_rows)
+    if n == 0:
+        raise CsffnError(_abi.ERR_INVALID_ARG, "csffn_moe_workspace_size")
+    return int(n)
+
+
+def moe_dispatch_workspace_size(max_rows: int, n_experts: int) -> int:
+    n = load().csffn_moe_dispatch_workspace_size(max_rows, n_experts)
+    if n == 0:
+        raise CsffnError(_abi.ERR_INVALID_ARG, "csffn_moe_dispatch_workspace_size")
+    return int(n)
+
+
+def new_moe_workspace(layer: MoELayer, max_rows: int) -> torch.Tensor:
+    """An initialised workspace for moe_ffn_forward and moe_dispatch of up to max_rows = T * k rows."""
+    ws = torch.empty(moe_workspace_size(layer, max_rows), dtype=torch.uint8, device=layer.w_gate.device)
+    with torch.cuda.device(ws.device):
+        workspace_init(ws)
+    return ws
+
+
+def new_moe_dispatch_workspace(max_rows: int, n_experts: int, device="cuda") -> torch.Tensor:
+    """A workspace for moe_dispatch alone (it needs no initialisation)."""
+    return torch.empty(moe_dispatch_workspace_size(max_rows, n_experts), dtype=torch.uint8, device=device)
+
+
+def moe_logits(x: torch.Tensor, w_router: torch.Tensor, logits: torch.Tensor, stream=None) -> None:
+    """logits [T, E] fp32 = x [T, d] . w_router [E, d]^T (bf16 operands, fp32 sums)."""
+    (T, d), (E, _) = _matrix(x, "x"), _matrix(w_router, "w_router")
+    c = _Call(x)
+    c.run("csffn_moe_logits", stream, c.ptr(x, "x", (T, d), _BF16), c.ptr(w_router, "w_router", (E, d), _BF16), T, E, d,
+          c.ptr(logits, "logits", (T, E), _F32))
+
+
+def moe_route(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, bias: Optional[torch.Tensor] = None,
+              score: int = _abi.ROUTE_SOFTMAX, renormalize: bool = True, scale: float = 1.0, stream=None) -> None:
+    """The k = ids.shape[1] experts of every token, by logits [T, E] (plus bias [E] for the choice
+    alone), and their weights; see csffn_moe_route."""
+    (T, E), (_, k) = _matrix(logits, "logits"), _matrix(ids, "ids")
+    c = _Call(logits)
+    c.run("csffn_moe_route", stream, c.ptr(logits, "logits", (T, E), _F32, _BF16), _CODE[logits.dtype],
+          c.ptr(bias, "bias", (E,), _F32), T, E, k, score, int(renormalize), scale, c.ptr(ids, "ids", (T, k), _I32),
+          c.ptr(weights, "weights", (T, k), _F32))
+
+
+def moe_dispatch(x: torch.Tensor, ids: torch.Tensor, offsets: torch.Tensor, order: torch.Tensor, pos: torch.Tensor,
+                 xs: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """Sorts the token slots by expert and gathers the tokens' rows into xs [T * k, d]; the number of
+    experts is offsets.shape[0] - 1.  See csffn_moe_dispatch."""
+    (T, d), (_, k) = _matrix(x, "x"), _matrix(ids, "ids")
+    E = offsets.numel() - 1
+    c = _Call(x)
+    c.run("csffn_moe_dispatch", stream, c.ptr(x, "x", (T, d), _BF16, _F32), _CODE[x.dtype],
+          c.ptr(ids, "ids", (T, k), _I32), T, k, E, d, c.ptr(offsets, "offsets", (E + 1,), _I32),
+          c.ptr(order, "order", (T * k,), _I32), c.ptr(pos, "pos", (T, k), _I32), c.ptr(xs, "xs", (T * k, d), x.dtype),
+          c.ws(ws), ws.numel())
+
+
+def moe_ffn_forward(layer: MoELayer, xs: torch.Tensor, offsets: torch.Tensor, ys: torch.Tensor, ws: torch.Tensor,
+                    stream=None) -> None:
+    """The experts' gated FFNs on the sorted rows xs [rows, d] -> ys [rows, d] (bf16); see
+    csffn_moe_ffn_forward.  ws: new_moe_workspace(layer, rows or more)."""
+    rows, _ = _matrix(xs, "xs")
+    c = _Call(xs)
+    if layer.w_gate.get_device() != c.index:
+        raise ValueError("the layer must be on the device of the rows")
+    c.run("csffn_moe_ffn_forward", stream, layer.ref(), c.ptr(xs, "xs", (rows, layer.d), _BF16),
+          c.ptr(offsets, "offsets", (layer.n_experts + 1,), _I32), rows, c.ptr(ys, "ys", (rows, layer.d), _BF16),
+          c.ws(ws), ws.numel())
+
+
+def moe_combine(ys: torch.Tensor, pos: torch.Tensor, weights: Optional[torch.Tensor], out: torch.Tensor,
+                out_mode: Optional[int] = None, stream=None) -> None:
+    """out [T, d] = sum over the token's slots of weights * ys[pos]; see csffn_moe_combine."""
+    (rows, d), (T, k) = _matrix(ys, "ys"), _matrix(pos, "pos")
+    if out_mode is None:
+        out_mode = _abi.OUT_BF16 if out.dtype == _BF16 else _abi.OUT_F32
+    c = _Call(out)
+    c.run("csffn_moe_combine", stream, c.ptr(ys, "ys", (rows, d), _BF16), c.ptr(pos, "pos", (T, k), _I32),
+          c.ptr(weights, "weights", (T, k), _F32), T, k, rows, d,
+          c.ptr(out, "out", (T, d), _BF16 if out_mode == _abi.OUT_BF16 else _F32), out_mode)
+
+
+def block_norm(h: torch.Tensor, y: Optional[torch.Tensor], h_out: Optional[torch.Tensor],
+               xn: Optional[torch.Tensor], g_post: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+               g_pre: Optional[torch.Tensor] = None, res_scale: float = 1.0, out_scale: float = 1.0,
+               eps: float = 1e-6, stream=None) -> None:
+    """h_out = res_scale * h + out_scale * gate * rms(y) * g_post, xn = rms(h_out) * g_pre; see
+    csffn_block_norm.  gate: [d] (per channel) or [T, d] (per token)."""
+    T, d = _matrix(h, "h")
+    per_token = gate is not None and gate.dim() == 2
+    c = _Call(h)
+    c.run("csffn_block_norm", stream, c.ptr(h, "h", (T, d), _F32), c.ptr(y, "y", (T, d), _BF16, _F32),
+          _abi.BF16 if y is None else _CODE[y.dtype], c.ptr(g_post, "g_post", (d,), _F32),
+          c.ptr(gate, "gate", (T, d) if per_token else (d,), _F32), T if per_token else 1,
+          c.ptr(g_pre, "g_pre", (d,), _F32), res_scale, out_scale, eps, T, d, c.ptr(h_out, "h_out", (T, d), _F32),
+          c.ptr(xn, "xn", (T, d), _BF16, _F32), _abi.BF16 if xn is None else _CODE[xn.dtype])
+
+
 # ------------------------------------------------------------------------------ buffers
 
 @dataclass

@@ -200,6 +200,85 @@ cudaError_t launch_rmsnorm_bf16(const float* h, int B, int d, float eps, void* x
 
 cudaError_t launch_timeout_selftest(uint64_t* flag, uint32_t* err, int spin_limit, cudaStream_t s);
 
+// ---------------------------------------------------------------------------------------------
+// Routed FFN (moe_route.cu, moe_sort.cu, moe_ffn.cu) and the norms around a block (block_norm.cu).
+// ---------------------------------------------------------------------------------------------
+struct MoeWs {          // workspace of csffn_moe_dispatch and csffn_moe_ffn_forward
+  size_t err;           // uint32 error word, where WsLayout has it (csffn_check_status)
+  size_t hist;          // dispatch: int32 [chunks][E] expert counts per chunk of slots
+  size_t v;             // ffn: bf16 [rows][h]
+  size_t total;
+};
+constexpr int kMoeChunk = 1024;     // least slots per counting chunk
+constexpr int kMoeMaxChunks = 256;  // most chunks: each placing CTA adds up all chunks' counts
+inline int moe_chunk_slots(int rows) {
+  const int per = (rows + kMoeMaxChunks - 1) / kMoeMaxChunks;
+  return per <= kMoeChunk ? kMoeChunk : (per + kMoeChunk - 1) / kMoeChunk * kMoeChunk;
+}
+inline int moe_chunks(int rows) { return (rows + moe_chunk_slots(rows) - 1) / moe_chunk_slots(rows); }
+MoeWs moe_ws_layout(int rows, int E, int h);  // h == 0: the dispatch's part alone
+
+cudaError_t launch_moe_logits(const void* x, const void* w, int T, int E, int d, float* logits, cudaStream_t s);
+
+struct RouteArgs {
+  const void* logits;
+  const float* bias;
+  int T, E, k, score, renorm;
+  float scale;
+  int32_t* ids;
+  float* weights;
+};
+cudaError_t launch_moe_route(const RouteArgs& a, int ldtype, cudaStream_t s);
+
+struct DispatchArgs {
+  const void* x;
+  const int32_t* ids;
+  int T, k, E;
+  int row_vecs;  // 16-byte vectors per row
+  int32_t* offsets;
+  int32_t* order;
+  int32_t* pos;
+  void* xs;
+  int32_t* hist;
+};
+cudaError_t launch_moe_dispatch(const DispatchArgs& a, cudaStream_t s);
+
+struct CombineArgs {
+  const void* ys;
+  const int32_t* pos;
+  const float* weights;
+  int T, k, rows, d;
+  void* out;
+  int out_mode;
+};
+cudaError_t launch_moe_combine(const CombineArgs& a, cudaStream_t s);
+
+struct MoeFfnArgs {
+  const void* W_gate;
+  const void* W_up;
+  const void* W_down_t;
+  const void* xs;
+  const int32_t* offsets;
+  int d, h, E, act, rows;
+  void* v;   // bf16 [rows, h]
+  void* ys;  // bf16 [rows, d]
+  uint32_t* err;
+};
+cudaError_t launch_moe_ffn(const MoeFfnArgs& a, cudaStream_t s);
+
+struct BlockNormArgs {
+  const float* h;
+  const void* y;
+  const float* g_post;
+  const float* gate;
+  const float* g_pre;
+  float* h_out;
+  void* xn;
+  int T, d, gate_per_token;
+  float res_scale, out_scale, eps;
+};
+cudaError_t launch_block_norm(const BlockNormArgs& a, int ydtype, int xdtype, cudaStream_t s);
+
 int sm_count();
 
 }  // namespace csffn

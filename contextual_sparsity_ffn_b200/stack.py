@@ -1,8 +1,9 @@
-"""Compositions of the library's entry points: a residual stack of sparse FFN layers and a Sirius
-round (sparse drafts, then the dense verify of the chunk).
+"""Compositions of the library's entry points: a residual stack of sparse FFN layers, a Sirius
+round (sparse drafts, then the dense verify of the chunk) and a residual stack of routed FFN layers.
 
 These only sequence C-ABI calls (csffn_rmsnorm_bf16, csffn_calibrate_threshold,
-csffn_dense_ffn_forward, csffn_cats_ffn_forward); every step of the arithmetic runs in the library.
+csffn_dense_ffn_forward, csffn_cats_ffn_forward, csffn_block_norm, csffn_moe_*); every step of the
+arithmetic runs in the library.
 
 Stack ("SVD Contextual Sparsity Predictors for Fast LLM Inference", Table 12: the LLaMA-3-8B FFN
 shape; the block structure is the plain reading): h <- h + FFN(bf16(RMSNorm(h))) per layer, the
@@ -13,6 +14,11 @@ that layer.
 Sirius round ("SIRIUS : Contexual Sparisty with Correction for Efficient LLMs", "Approach"): the
 sparse FFN drafts the chunk's tokens one at a time, then the full FFN (same weights) runs on the
 whole chunk at once.
+
+Routed stack (moe_stack): h <- res_scale h + out_scale gate * (rms(y) g_post) per layer, y the routed
+FFN of rms(h) g_pre: the router picks k of the layer's experts for each token, the tokens are sorted
+by expert, each expert's gated FFN runs on its rows, and the results come back weighted.  Any number
+of tokens (a decode step or a prompt); nothing leaves the device, so a step can be captured.
 """
 from __future__ import annotations
 
@@ -111,3 +117,76 @@ def round_effective_density(counts, h: int) -> float:
     ``counts``: the drafts' n_t.  (sum_t (h + 2 n_t) + 3 h) / (3 h T)."""
     T = len(counts)
     return (sum(h + 2.0 * n for n in counts) + 3.0 * h) / (3.0 * h * T)
+
+
+# ------------------------------------------------------------------------------ routed FFN stack
+
+@dataclass
+class MoEBlock:
+    """One routed FFN layer of the stack: experts, router, and the norms around it (fp32 vectors)."""
+
+    experts: cs.MoELayer
+    w_router: torch.Tensor                      # bf16 [n_experts, d]
+    k: int                                      # experts per token
+    g_pre: Optional[torch.Tensor] = None        # [d] gain of the norm before the block
+    g_post: Optional[torch.Tensor] = None       # [d] gain of the norm of its output; None: no such norm
+    gate: Optional[torch.Tensor] = None         # [d] or [T, d] gate of its output
+    sel_bias: Optional[torch.Tensor] = None     # [n_experts] added to the logits for the choice alone
+    score: int = _abi.ROUTE_SOFTMAX
+    renormalize: bool = True
+    route_scale: float = 1.0
+    res_scale: float = 1.0
+    out_scale: float = 1.0
+
+
+@dataclass
+class MoEBuffers:
+    """Device buffers of routed layers of one shape for T tokens."""
+
+    xn: torch.Tensor        # bf16 [T, d]: the layer's input
+    logits: torch.Tensor    # fp32 [T, n_experts]
+    ids: torch.Tensor       # int32 [T, k]
+    weights: torch.Tensor   # fp32 [T, k]
+    offsets: torch.Tensor   # int32 [n_experts + 1]
+    order: torch.Tensor     # int32 [T * k]
+    pos: torch.Tensor       # int32 [T, k]
+    xs: torch.Tensor        # bf16 [T * k, d]: the rows by expert
+    ys: torch.Tensor        # bf16 [T * k, d]: the experts' outputs
+    y: torch.Tensor         # bf16 [T, d]: the layer's output
+    ws: torch.Tensor
+
+    @classmethod
+    def new(cls, block: MoEBlock, T: int) -> "MoEBuffers":
+        L, k, dev = block.experts, block.k, block.w_router.device
+
+        def empty(*shape, dtype):
+            return torch.empty(*shape, dtype=dtype, device=dev)
+        bf, i32 = torch.bfloat16, torch.int32
+        return cls(xn=empty(T, L.d, dtype=bf), logits=empty(T, L.n_experts, dtype=torch.float32),
+                   ids=empty(T, k, dtype=i32), weights=empty(T, k, dtype=torch.float32),
+                   offsets=empty(L.n_experts + 1, dtype=i32), order=empty(T * k, dtype=i32), pos=empty(T, k, dtype=i32),
+                   xs=empty(T * k, L.d, dtype=bf), ys=empty(T * k, L.d, dtype=bf), y=empty(T, L.d, dtype=bf),
+                   ws=cs.new_moe_workspace(L, T * k))
+
+
+def moe_layer(block: MoEBlock, x: torch.Tensor, y: torch.Tensor, buf: MoEBuffers) -> None:
+    """y [T, d] = the routed FFN of x [T, d] (bf16): router, sort, experts, weighted sum."""
+    cs.moe_logits(x, block.w_router, buf.logits)
+    cs.moe_route(buf.logits, buf.ids, buf.weights, bias=block.sel_bias, score=block.score,
+                 renormalize=block.renormalize, scale=block.route_scale)
+    cs.moe_dispatch(x, buf.ids, buf.offsets, buf.order, buf.pos, buf.xs, buf.ws)
+    cs.moe_ffn_forward(block.experts, buf.xs, buf.offsets, buf.ys, buf.ws)
+    cs.moe_combine(buf.ys, buf.pos, buf.weights, y)
+
+
+def moe_stack(blocks: List[MoEBlock], h: torch.Tensor, buf: MoEBuffers) -> None:
+    """One pass of h [T, d] (fp32, updated in place) through routed layers of one shape: the norm
+    before the first layer, then for each layer its routed FFN and one pass that norms its output,
+    updates h and norms the next layer's input."""
+    cs.block_norm(h, None, None, buf.xn, g_pre=blocks[0].g_pre, eps=RMS_EPS)
+    for i, b in enumerate(blocks):
+        moe_layer(b, buf.xn, buf.y, buf)
+        last = i + 1 == len(blocks)
+        cs.block_norm(h, buf.y, h, None if last else buf.xn, g_post=b.g_post, gate=b.gate,
+                      g_pre=None if last else blocks[i + 1].g_pre, res_scale=b.res_scale, out_scale=b.out_scale,
+                      eps=RMS_EPS)

@@ -310,6 +310,107 @@ csffn_status csffn_sparse_ffn_forward_static(const csffn_layer* layer, const voi
                                              const int32_t* idx, const int32_t* count, const float* a_val,
                                              void* out, int out_mode, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Routed FFN (mixture of experts) and the norms around a block.
+ *
+ * A routed FFN layer holds E gated FFNs (experts); a router picks k of them for every token and
+ * their outputs are summed with the router's weights.  One layer step is
+ *   csffn_block_norm -> csffn_moe_logits -> csffn_moe_route -> csffn_moe_dispatch ->
+ *   csffn_moe_ffn_forward -> csffn_moe_combine.
+ * These calls take any number of tokens (decode steps and prompts).  Every count that depends on
+ * the routing stays on the device, so the whole step can be captured in a CUDA graph.  All of them
+ * are bit-for-bit repeatable.  Pointers, streams, errors and workspaces as above; T == 0 (or
+ * rows == 0) is an empty call.
+ * --------------------------------------------------------------------------------------------- */
+#define CSFFN_MAX_EXPERTS 512
+#define CSFFN_MAX_TOPK 16
+#define CSFFN_MAX_MOE_ROWS (1 << 22) /* tokens x experts per token */
+
+/* One routed FFN layer, bf16.  Expert e's matrices are neuron-major like csffn_layer's. */
+typedef struct {
+  int32_t d;              /* model width, a multiple of 8 */
+  int32_t h;              /* neurons per expert, a multiple of 8 */
+  int32_t n_experts;      /* 1 .. CSFFN_MAX_EXPERTS */
+  int32_t act;            /* csffn_act */
+  const void* w_gate;     /* [n_experts, h, d] bf16 */
+  const void* w_up;       /* [n_experts, h, d] bf16 */
+  const void* w_down_t;   /* [n_experts, h, d] bf16 */
+} csffn_moe_layer;
+
+/* How csffn_moe_route turns the selected logits into weights. */
+typedef enum { CSFFN_ROUTE_SOFTMAX = 0, CSFFN_ROUTE_SIGMOID = 1 } csffn_route_score;
+
+/* Router projection: logits[t, e] = sum_c x[t, c] * w_router[e, c], fp32 sums.
+ *   x: bf16 [T, d]; w_router: bf16 [E, d]; logits: fp32 [T, E].  d % 8 == 0, both 16-byte aligned. */
+csffn_status csffn_moe_logits(const void* x, const void* w_router, int T, int E, int d, float* logits,
+                              void* stream);
+
+/* Router selection.  key[t, e] = logits[t, e] (+ sel_bias[e], one fp32 addition, when not NULL).
+ *   ids[t, 0 .. k) = the k experts with the largest keys, largest first, equal keys by the lower
+ *   expert.  A key of -inf or NaN is never selected: when fewer than k experts are left, the
+ *   remaining entries are ids = -1 with weight 0.
+ *   weights[t, j] = scale * s_j from the selected logits l_j (without the bias):
+ *     SOFTMAX: exp(l_j) / sum exp(l), the sum over all experts, or over the selected ones with
+ *              renormalize != 0.  NaN logits count as -inf; +inf logits share the whole weight.
+ *     SIGMOID: 1 / (1 + exp(-l_j)), with renormalize != 0 divided by the selected ones' sum (at
+ *              least 1e-20).
+ *   logits: [T, E] in ldtype (csffn_dtype); sel_bias: fp32 [E] or NULL; ids: int32 [T, k];
+ *   weights: fp32 [T, k].  1 <= k <= min(E, CSFFN_MAX_TOPK). */
+csffn_status csffn_moe_route(const void* logits, int ldtype, const float* sel_bias, int T, int E, int k, int score,
+                             int renormalize, float scale, int32_t* ids, float* weights, void* stream);
+
+/* Workspace bytes of csffn_moe_dispatch for up to max_rows = T * k slots (0 for invalid arguments).
+ * A workspace of csffn_moe_workspace_size(layer, max_rows) is large enough too. */
+size_t csffn_moe_dispatch_workspace_size(int max_rows, int n_experts);
+
+/* Tokens sorted by expert.  Slot s = t * k + j holds token t's j-th expert ids[t, j]; slots whose
+ * id is outside [0, E) (padding) are dropped.  The other slots are sorted by expert, slots of one
+ * expert in slot order:
+ *   offsets[e] = slots of experts below e (int32 [E + 1]; offsets[E] = slots kept);
+ *   order[p] = slot at sorted position p (int32 [T * k]); pos[s] = sorted position of slot s, or -1
+ *   (int32 [T, k]); xs[p, :] = x[order[p] / k, :] ([T * k, d] in xdtype).
+ *   Entries of order and rows of xs at and behind offsets[E] are left as they were.
+ *   x: [T, d] in xdtype (csffn_dtype).  1 <= k <= CSFFN_MAX_TOPK, 1 <= E <= CSFFN_MAX_EXPERTS.
+ *   T == 0: writes offsets = 0. */
+csffn_status csffn_moe_dispatch(const void* x, int xdtype, const int32_t* ids, int T, int k, int E, int d,
+                                int32_t* offsets, int32_t* order, int32_t* pos, void* xs, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/* Workspace bytes of csffn_moe_ffn_forward for up to max_rows rows (0 for invalid arguments).
+ * Initialise it once with csffn_workspace_init; csffn_check_status reports its error word. */
+size_t csffn_moe_workspace_size(const csffn_moe_layer* layer, int max_rows);
+
+/* The experts' gated FFNs on sorted rows: for expert e and its rows p in [offsets[e], offsets[e+1]),
+ *   ys[p, :] = sum_i v[p, i] * W_down^T[e, i, :],  v[p, i] = act(xs_p . W_gate[e, i, :]) * (xs_p . W_up[e, i, :]).
+ *   xs: bf16 [rows, d]; offsets: int32 [n_experts + 1] on the device, ascending, as
+ *   csffn_moe_dispatch writes it (values are clamped to 0 .. rows and to ascending order); ys: bf16
+ *   [rows, d]; rows at and behind offsets[n_experts] are left as they were.  xs and ys must not
+ *   overlap.  Sums are fp32; v is rounded once to bf16 for the down projection. */
+csffn_status csffn_moe_ffn_forward(const csffn_moe_layer* layer, const void* xs, const int32_t* offsets, int rows,
+                                   void* ys, void* ws, size_t ws_bytes, void* stream);
+
+/* Expert outputs back in token order: out[t, :] = sum_j weights[t, j] * ys[pos[t, j], :] in fp32,
+ * written (or accumulated) by out_mode; entries with pos outside [0, rows) are skipped, whatever
+ * their weight.  ys: bf16 [rows, d]; pos: int32 [T, k]; weights: fp32 [T, k], or NULL for weights
+ * of 1; out: [T, d] in the dtype of out_mode. */
+csffn_status csffn_moe_combine(const void* ys, const int32_t* pos, const float* weights, int T, int k, int rows, int d,
+                               void* out, int out_mode, void* stream);
+
+/* The norms around a block, fused with its gate and residual scale.  With rms(r) = r / sqrt(mean(r^2)
+ * + eps) over a row:
+ *   u  = rms(y) * g_post          (u = y when g_post is NULL)
+ *   h' = res_scale * h + out_scale * gate * u      (gate 1 when NULL)
+ *   xn = rms(h') * g_pre          (not computed when xn is NULL; g_pre NULL is a gain of 1)
+ *   y NULL: no block output yet, h' = res_scale * h (the norm before the first block).
+ * h: fp32 [T, d], the residual stream; y: [T, d] in ydtype, the block's output; g_post, g_pre: fp32
+ * [d]; gate: fp32 [d] (gate_rows == 1, a gate per channel) or [T, d] (gate_rows == T, per token);
+ * h_out: fp32 [T, d] (may be h itself; NULL: h' is not written); xn: [T, d] in xdtype, the next
+ * block's input, which must not overlap h or h_out.  At least one of h_out and xn.  d % 8 == 0,
+ * d <= CSFFN_MAX_D, pointers 16-byte aligned. */
+csffn_status csffn_block_norm(const float* h, const void* y, int ydtype, const float* g_post, const float* gate,
+                              int gate_rows, const float* g_pre, float res_scale, float out_scale, float eps, int T,
+                              int d, float* h_out, void* xn, int xdtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
