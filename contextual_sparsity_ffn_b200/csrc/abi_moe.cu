@@ -12,12 +12,17 @@ namespace csffn {
 MoeWs moe_ws_layout(int rows, int E, int h) {
   MoeWs L;
   L.err = ws_layout(8, 1, 1, 0).err;
-  size_t o = 1024;
+  L.ctr = 1024;  // fixed: calls of fewer rows must not write where the counters of larger ones are
+  size_t o = L.ctr + align_up(sizeof(uint32_t) * 2 * kMoeMaxPairs * 2, 256);
   L.hist = o;
   L.v = o;  // the dispatch's counts and the experts' v are never live at once
-  const size_t hist = sizeof(int32_t) * (size_t)moe_chunks(rows) * E;
+  // the most chunks any call of up to `rows` slots has
+  const int chunks = (rows + kMoeChunk - 1) / kMoeChunk;
+  const size_t hist = sizeof(int32_t) * (size_t)(chunks < kMoeMaxChunks ? chunks : kMoeMaxChunks) * E;
   const size_t v = sizeof(bf16) * (size_t)rows * h;
   o += align_up(hist > v ? hist : v, 256);
+  L.part = o;
+  if (h > 0) o += sizeof(float) * moe_part_floats(rows);
   L.total = o;
   return L;
 }
@@ -154,6 +159,8 @@ csffn_status csffn_moe_ffn_forward(const csffn_moe_layer* layer, const void* xs,
   a.act = layer->act;
   a.rows = rows;
   a.v = at<void>(ws, L.v);
+  a.part = at<float>(ws, L.part);
+  a.ctr = at<uint32_t>(ws, L.ctr);
   a.ys = ys;
   a.err = at<uint32_t>(ws, L.err);
   return cuda_status(launch_moe_ffn(a, as_stream(stream)));

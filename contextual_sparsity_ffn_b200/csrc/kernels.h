@@ -206,9 +206,15 @@ cudaError_t launch_timeout_selftest(uint64_t* flag, uint32_t* err, int spin_limi
 struct MoeWs {          // workspace of csffn_moe_dispatch and csffn_moe_ffn_forward
   size_t err;           // uint32 error word, where WsLayout has it (csffn_check_status)
   size_t hist;          // dispatch: int32 [chunks][E] expert counts per chunk of slots
+  size_t ctr;           // ffn: uint32 [2 kernels][kMoeMaxPairs][2] split tiles' counters, zero between calls
   size_t v;             // ffn: bf16 [rows][h]
+  size_t part;          // ffn: fp32 split tiles' parts, moe_part_floats(rows)
   size_t total;
 };
+constexpr int kMoeTileRows = 256;  // most rows of one expert per tile
+constexpr int kMoeMaxPairs = 80;   // most CTA pairs at work
+constexpr int kMoeFewRows = 64;    // tiles this low may be parts of two tiles per pair
+inline int moe_part_rows(int rows) { return rows >= kMoeTileRows ? kMoeTileRows : (rows + 31) / 32 * 32; }
 constexpr int kMoeChunk = 1024;     // least slots per counting chunk
 constexpr int kMoeMaxChunks = 256;  // most chunks: each placing CTA adds up all chunks' counts
 inline int moe_chunk_slots(int rows) {
@@ -216,6 +222,11 @@ inline int moe_chunk_slots(int rows) {
   return per <= kMoeChunk ? kMoeChunk : (per + kMoeChunk - 1) / kMoeChunk * kMoeChunk;
 }
 inline int moe_chunks(int rows) { return (rows + moe_chunk_slots(rows) - 1) / moe_chunk_slots(rows); }
+inline size_t moe_part_floats(int rows) {  // [places][2 CTAs][2 accumulators][rows of a tile][128]
+  const int n = moe_part_rows(rows);  // a workspace for more rows also serves fewer
+  const int all = n <= 2 * kMoeFewRows ? 2 * kMoeMaxPairs * (n < kMoeFewRows ? n : kMoeFewRows) : kMoeMaxPairs * n;
+  return (size_t)all * 2 * 2 * 128;
+}
 MoeWs moe_ws_layout(int rows, int E, int h);  // h == 0: the dispatch's part alone
 
 cudaError_t launch_moe_logits(const void* x, const void* w, int T, int E, int d, float* logits, cudaStream_t s);
@@ -261,6 +272,8 @@ struct MoeFfnArgs {
   const int32_t* offsets;
   int d, h, E, act, rows;
   void* v;   // bf16 [rows, h]
+  float* part;
+  uint32_t* ctr;
   void* ys;  // bf16 [rows, d]
   uint32_t* err;
 };

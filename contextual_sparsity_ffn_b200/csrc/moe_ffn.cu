@@ -1,135 +1,623 @@
-// Router projection and the experts' gated FFNs on rows sorted by expert.
+// The experts' gated FFNs on rows sorted by expert, on the fifth-generation tensor cores.
 //
-// Plain tiled kernels: a CTA of 256 threads computes a tile of 64 rows x 64 outputs of one expert,
-// 4 x 4 outputs per thread, the contraction in steps of 32 through shared memory, fp32 FMA.
+//   gate/up: v[p, i] = act(xs_p . W_gate[e, i]) * (xs_p . W_up[e, i])      (bf16 into the workspace)
+//   down:    ys[p, c] = sum_i v[p, i] W_down^T[e, i, c]
+//
+// Both kernels compute D[output, row] with the weights as the M side: a tile is 256 outputs
+// (neurons, or columns of ys) x up to 256 rows of one expert, and a pair of CTAs works on it
+// (cta_group::2, M = 256: 128 outputs each).  The rows are the N side because an expert's row count
+// is whatever the router made it: N is any multiple of 32 up to 256 chosen per tile, so a ragged
+// expert wastes at most 31 rows of multiplication and none of the weight traffic.
+//
+// Work split: whole tiles go round the pairs as long as there is one for every pair.  The R tiles
+// left over (all of them in a decode step) would leave pairs idle, so they are cut along the
+// contraction.  Up to half as many tiles as pairs: each into S = pairs / R parts (at most kMaxParts),
+// one part per pair.  More, with few rows: the tiles' k-blocks, in order, form one run that is
+// divided evenly among the pairs (a pair holds parts of at most two tiles).  A pair with a part
+// stores its fp32 accumulators in the workspace and counts up the tile's counter; the last one adds
+// the parts in their order (the same bits whoever is last), writes the tile and clears the counter.
+// No pair waits for another.
+//
+// Row split: an expert with n rows takes ceil(n / 256) tiles of equal height (rounded up to 32).
+// Tiles are numbered expert by expert, output block by output block, row tiles innermost, so the
+// pairs at work at one time share weight blocks and an expert's rows through L2.
+//
+// Operands come by TMA tensor copies with the 128-byte swizzle, 64 contraction elements per stage:
+// W_gate and W_up 128 x 64 each (gate/up, K-major) or W_down^T as two boxes of 64 columns x 64
+// neurons (down, MN-major), and half the tile's rows in each CTA.  All copies of a stage complete on
+// one barrier of the pair's even CTA, whose MMA warp issues for both.  Accumulators: two buffers, one
+// drained while the next tile accumulates: 256 TMEM columns each (down), or 128 columns each of gate
+// and of up; a gate/up tile of more than 128 rows takes both.
+//
+// Warp roles (320 threads): warp 0 issues the copies, warp 1 owns TMEM and (even CTA) issues the
+// MMAs, warps 2-9 run the epilogue: TMEM lane = output, column = row, two warps per lane quarter, each
+// half of the columns.  Neighbouring lanes exchange one value of each column pair so that a lane
+// stores two adjacent outputs (4 bytes).
+//
+// Row bounds come from the device: `offsets` is clamped to 0 .. rows and to ascending order when it is
+// read, so no offsets can lead an access outside the buffers.  Every wait is bounded (one second)
+// and records the timeout.
 #include "common.cuh"
+#include "fused_end.cuh"
 #include "kernels.h"
 #include "tcgen05.cuh"
 
 namespace csffn {
 namespace {
 
-constexpr int kT = 64, kK = 32, kThreads = 256;
+constexpr int kThreads = 320;
+constexpr int kEpiWarps = 8;
+constexpr int kMaxN = kMoeTileRows;                   // rows per tile
+constexpr int kKB = 64;                               // contraction elements per stage
+constexpr uint32_t kWBox = 128 * kKB * 2;             // one CTA's 128 outputs x 64: 16 KB
+constexpr uint32_t kRowsMax = (kMaxN / 2) * kKB * 2;  // one CTA's half of the rows: 16 KB
+constexpr int kMaxParts = 8, kMaxPartsHigh = 4;       // parts of a tile of at most / more than 64 rows
+constexpr uint32_t kUpCol = 256;                      // TMEM column of the up accumulator / second buffer
 
-enum { kGateUp = 0, kDown = 1, kLogits = 2 };
-
-struct TileArgs {
-  const bf16* a;        // rows [n, K]
-  const bf16* w0;       // [E, N, K] (gate, router) or [E, K, N] (down)
-  const bf16* w1;       // up
-  const int32_t* offsets;  // NULL: one group of n rows
-  int n, N, K, E, act;
-  void* out;            // [n, N]
+template <bool kDown>
+struct Cfg {
+  static constexpr uint32_t kW = kDown ? kWBox : 2 * kWBox;
+  static constexpr uint32_t kStage = kW + kRowsMax;
+  static constexpr int kStages = kDown ? 6 : 4;
+  static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
 };
 
-template <int MODE>
-__global__ void __launch_bounds__(kThreads) tile_kernel(const TileArgs p) {
-  __shared__ float sa[kT][kK + 1], s0[kT][kK + 1], s1[MODE == kGateUp ? kT : 1][kK + 1];
-  pdl_trigger();
-  pdl_wait_prior();
-  // this row tile's expert and rows
-  int e = 0, r0 = 0, r1 = 0, left = blockIdx.y;
-  bool found = false;
-  int lo = 0;
-  for (e = 0; e < p.E; ++e) {
-    int hi = p.n;
-    if (p.offsets) {
-      if (e == 0) lo = min(max(p.offsets[0], 0), p.n);
-      hi = max(lo, min(max(p.offsets[e + 1], 0), p.n));
-    }
-    const int tiles = (hi - lo + kT - 1) / kT;
-    if (left < tiles) {
-      r0 = lo + left * kT;
-      r1 = min(hi, r0 + kT);
-      found = true;
-      break;
-    }
-    left -= tiles;
-    lo = hi;
+struct Args {
+  const int32_t* offsets;
+  int rows, E, N, K, act;  // N outputs per expert, K contraction
+  bf16* out;               // [rows, N]
+  float* part;             // [places][2 CTAs][accumulators][part_n / 4][128][4] split tiles' parts
+  int part_n;              // most rows of a tile of this call
+  int max_parts;
+  bool few_rows;
+  uint32_t* ctr;           // [pairs][2]: parts done of the split tiles
+  uint32_t* err;
+};
+
+// Every expert's rows and tiles, worked out once per CTA: lo[e] .. lo[e + 1] are expert e's rows,
+// tp[e] the row tiles of the experts before it.
+struct Plan {
+  int lo[CSFFN_MAX_EXPERTS + 1];
+  int tp[CSFFN_MAX_EXPERTS + 1];
+};
+
+// By one warp, from the raw offsets in p->lo: each lane takes a few consecutive entries.
+__device__ void make_plan(const Args& a, Plan* p) {
+  const int lane = threadIdx.x & 31, per = (a.E + kWarp) / kWarp;  // E + 1 entries
+  const int e0 = min(lane * per, a.E + 1), e1 = min(e0 + per, a.E + 1);
+  int top = 0;  // the largest offset up to here: ascending order
+  for (int e = e0; e < e1; ++e) {
+    top = max(top, min(p->lo[e], a.rows));
+    p->lo[e] = top;
   }
-  if (!found) return;
-  const int c0 = blockIdx.x * kT;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  const size_t wbase = (size_t)e * p.N * p.K;
-  float acc0[4][4] = {}, acc1[4][4] = {};
-  for (int k0 = 0; k0 < p.K; k0 += kK) {
-    for (int i = threadIdx.x; i < kT * kK; i += kThreads) {
-      const int r = i / kK, k = i % kK;
-      sa[r][k] = r0 + r < r1 && k0 + k < p.K ? __bfloat162float(p.a[(size_t)(r0 + r) * p.K + k0 + k]) : 0.f;
-      if (MODE == kDown) {
-        const int kk = i / kT, c = i % kT;
-        s0[c][kk] = c0 + c < p.N && k0 + kk < p.K ? __bfloat162float(p.w0[wbase + (size_t)(k0 + kk) * p.N + c0 + c]) : 0.f;
-      } else {
-        const bool in = c0 + r < p.N && k0 + k < p.K;
-        s0[r][k] = in ? __bfloat162float(p.w0[wbase + (size_t)(c0 + r) * p.K + k0 + k]) : 0.f;
-        if (MODE == kGateUp) s1[r][k] = in ? __bfloat162float(p.w1[wbase + (size_t)(c0 + r) * p.K + k0 + k]) : 0.f;
-      }
+#pragma unroll
+  for (int o = 1; o < kWarp; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, top, o);
+    if (lane >= o) top = max(top, u);
+  }
+  int before = __shfl_up_sync(0xffffffffu, top, 1);  // of the entries of lower lanes
+  if (lane == 0) before = 0;
+  // entry e closes expert e - 1
+  int tiles = 0, prev = before;
+  for (int e = e0; e < e1; ++e) {
+    const int v = max(p->lo[e], before);
+    p->lo[e] = v;
+    if (e > 0) tiles += (v - prev + kMaxN - 1) / kMaxN;
+    p->tp[e] = tiles;
+    prev = v;
+  }
+  int sum = tiles;
+#pragma unroll
+  for (int o = 1; o < kWarp; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += u;
+  }
+  for (int e = e0; e < e1; ++e) p->tp[e] += sum - tiles;
+}
+
+struct Tile {
+  int e, m;        // expert, output block
+  int row0, row1;  // rows
+  int n;           // N of its MMAs: the rows rounded up to 32
+  bool once;       // the expert's weights are read by this row tile alone
+};
+
+__device__ __forceinline__ Tile find_tile(const Plan& p, int E, int mb, int i) {
+  const int q = i / mb;
+  int a = 0, b = E;  // tp[a] <= q < tp[b]
+  while (b - a > 1) {
+    const int c = (a + b) >> 1;
+    if (p.tp[c] <= q)
+      a = c;
+    else
+      b = c;
+  }
+  const int nt = p.tp[a + 1] - p.tp[a], r = i - p.tp[a] * mb;
+  const int cnt = p.lo[a + 1] - p.lo[a];
+  const int height = ((cnt + nt - 1) / nt + 31) / 32 * 32;
+  Tile t;
+  t.e = a;
+  t.m = r / nt;
+  t.row0 = p.lo[a] + (r % nt) * height;
+  t.row1 = min(t.row0 + height, p.lo[a + 1]);
+  t.n = (t.row1 - t.row0 + 31) / 32 * 32;
+  t.once = nt == 1;
+  return t;
+}
+
+// The work of one pair in order: (tile, k-blocks [kb0, kb1)).
+struct Items {
+  int pair, pairs, n_kb, n_whole, left;  // tiles [0, n_whole) go round whole, `left` after them
+  int split;                             // parts of a left-over tile, or 0: one run for all of them
+  int next;                              // next whole tile
+  int it, it1;                           // this pair's k-blocks of the run
+  int tile, kb0, kb1;                    // the current item
+  __device__ Items(int pair_, int pairs_, int n_kb_, int n_tiles, int max_parts, bool few_rows)
+      : pair(pair_), pairs(pairs_), n_kb(n_kb_) {
+    n_whole = n_tiles / pairs * pairs;
+    left = n_tiles - n_whole;
+    split = left ? min(min(pairs / left, max_parts), n_kb) : 1;
+    if (split == 1 && left > 0 && few_rows && n_kb >= 4) split = 0;
+    next = pair;
+    it = split == 0 ? run_start(pair) : 0;
+    it1 = split == 0 ? run_start(pair + 1) : 0;
+  }
+  // the run: left * n_kb k-blocks, more than half as many tiles as pairs, so no pair's share is empty
+  __device__ int run_start(int q) const { return (int)((long long)q * left * n_kb / pairs); }
+  __device__ int run_owner(int j) const { return (int)(((long long)(j + 1) * pairs - 1) / (left * n_kb)); }
+  __device__ bool advance() {
+    kb0 = 0;
+    kb1 = n_kb;
+    tile = next;
+    if (next < n_whole) {
+      next += pairs;
+      return true;
     }
-    __syncthreads();
-#pragma unroll 8
-    for (int k = 0; k < kK; ++k) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x = sa[ty + 16 * i][k];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc0[i][j] = fmaf(x, s0[tx + 16 * j][k], acc0[i][j]);
-          if (MODE == kGateUp) acc1[i][j] = fmaf(x, s1[tx + 16 * j][k], acc1[i][j]);
+    if (split == 0) {
+      if (it >= it1) return false;
+      tile = n_whole + it / n_kb;
+      kb0 = it % n_kb;
+      kb1 = min(n_kb, kb0 + (it1 - it));
+      it += kb1 - kb0;
+      return true;
+    }
+    const int q = next - n_whole;  // this pair's number, until its last item is out
+    if (q >= left * split) return false;
+    next = 0x7fffffff;
+    tile = n_whole + q % left;
+    kb0 = (q / left) * n_kb / split;
+    kb1 = (q / left + 1) * n_kb / split;
+    return true;
+  }
+  __device__ bool whole() const { return kb1 - kb0 == n_kb; }
+  __device__ int left_tile() const { return tile - n_whole; }
+  // the parts of the current tile, and where part r is kept (at most 2 * pairs places)
+  __device__ int first_pair() const { return run_owner(left_tile() * n_kb); }
+  __device__ int parts() const { return split ? split : run_owner(left_tile() * n_kb + n_kb - 1) - first_pair() + 1; }
+  __device__ int place(int r) const {
+    if (split) return left_tile() * split + r;
+    const int q = first_pair() + r;
+    return 2 * q + (run_start(q) >= left_tile() * n_kb ? 0 : 1);
+  }
+  __device__ int my_place() const {
+    if (split) return left_tile() * split + pair / left;
+    return 2 * pair + (run_start(pair) >= left_tile() * n_kb ? 0 : 1);
+  }
+};
+
+// Which accumulator buffers an item takes, and how often each was taken before: every role counts the
+// same items, so they agree on the barriers' phases.
+template <bool kDown>
+struct Buffers {
+  int turn = 0;
+  uint32_t used[2] = {0, 0};
+  int b;      // first buffer of the item
+  bool both;  // it takes both
+  __device__ void take(int n) {
+    both = !kDown && n > 128;
+    b = both ? 0 : turn;
+    if (!both) turn ^= 1;
+  }
+  __device__ void done() {
+    ++used[b];
+    if (both) ++used[1];
+  }
+  __device__ uint32_t column() const { return kDown ? 256u * b : 128u * b; }
+};
+
+struct Ring {
+  int slot = 0;
+  uint32_t round = 0;
+  __device__ void next(int n) {
+    if (++slot == n) {
+      slot = 0;
+      ++round;
+    }
+  }
+};
+
+// SiLU for a value that is rounded to bf16 next: the fast exponential and division (a few fp32
+// steps) are far below that rounding.
+__device__ __forceinline__ float act_fast(float z, int act) {
+  return act == CSFFN_ACT_SILU ? __fdividef(z, 1.0f + __expf(-z)) : fmaxf(z, 0.0f);
+}
+
+template <bool kDown>
+__global__ void __launch_bounds__(kThreads, 1)
+    pair_kernel(const Args a, const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ CUtensorMap tm_w1,
+                const __grid_constant__ CUtensorMap tm_r64, const __grid_constant__ CUtensorMap tm_r16) {
+  using C = Cfg<kDown>;
+  constexpr int kStages = C::kStages;
+  extern __shared__ __align__(1024) unsigned char moe_raw[];
+  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], accf[2], acce[2], drain;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ bool s_last;
+  __shared__ Plan s_plan;
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(moe_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int mb = (a.N + 255) / 256, n_kb = (a.K + kKB - 1) / kKB;
+
+  if (threadIdx.x == 0) {
+    tma_prefetch_map(&tm_w0);
+    if (!kDown) tma_prefetch_map(&tm_w1);
+    tma_prefetch_map(&tm_r64);
+    tma_prefetch_map(&tm_r16);
+    s_abort = 0;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&accf[i], 1);
+      mbar_init(&acce[i], 2 * kEpiWarps);
+    }
+    mbar_init(&drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&s_tmem, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers and TMEM are set up
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  // The gate/up kernel lets the down kernel start only after its own wait, so what came before the
+  // gate/up kernel is complete when the down kernel starts: the offsets (and the weights) may be read
+  // before the down kernel's wait, v after it.
+  if (!kDown) pdl_wait_prior();
+  pdl_trigger();
+  for (int e = threadIdx.x; e <= a.E; e += kThreads) s_plan.lo[e] = __ldcg(a.offsets + e);
+  __syncthreads();
+  if (warp == 0) make_plan(a, &s_plan);
+  __syncthreads();
+  const int n_tiles = s_plan.tp[a.E] * mb;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---- producer
+      Ring r;
+      long long issued = 0;
+      bool ok = true;
+      auto weights = [&](const Tile& t, int kb, unsigned char* st, uint32_t bar) {
+        const int out0 = t.m * 256 + (int)rank * 128;
+        if constexpr (kDown) {
+          tma_load_3d_pair(st, &tm_w0, out0, kb * kKB, t.e, bar);
+          tma_load_3d_pair(st + kWBox / 2, &tm_w0, out0 + 64, kb * kKB, t.e, bar);
+        } else {
+          tma_load_3d_pair(st, &tm_w0, kb * kKB, out0, t.e, bar);
+          tma_load_3d_pair(st + kWBox, &tm_w1, kb * kKB, out0, t.e, bar);
+        }
+      };
+      auto rows = [&](const Tile& t, int kb, unsigned char* st, uint32_t bar) {
+        const int half = t.n / 2, row0 = t.row0 + (int)rank * half;
+        int n = 0;
+        for (; n + 64 <= half; n += 64) tma_load_2d_pair(st + C::kW + n * (kKB * 2), &tm_r64, kb * kKB, row0 + n, bar);
+        for (; n < half; n += 16) tma_load_2d_pair(st + C::kW + n * (kKB * 2), &tm_r16, kb * kKB, row0 + n, bar);
+      };
+      auto expect = [&](const Tile& t, int slot) {
+        if (rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * (C::kW + (uint32_t)(t.n / 2) * (kKB * 2)));
+      };
+      Items w(pair, pairs, n_kb, n_tiles, a.max_parts, a.few_rows);
+      bool more = w.advance();
+      int first = 0;  // stages of the first item whose weights went out before the wait
+      if (kDown && more) {
+        const Tile t = find_tile(s_plan, a.E, mb, w.tile);
+        first = min(kStages, w.kb1 - w.kb0);
+        for (int q = 0; q < first; ++q) {
+          expect(t, q);
+          weights(t, w.kb0 + q, smem + (size_t)q * C::kStage, map_to_rank(&full[q], 0));
         }
       }
+      if (kDown) pdl_wait_prior();
+      for (; ok && more; more = w.advance()) {
+        const Tile t = find_tile(s_plan, a.E, mb, w.tile);
+        for (int kb = w.kb0; kb < w.kb1; ++kb, ++issued) {
+          unsigned char* st = smem + (size_t)r.slot * C::kStage;
+          const uint32_t bar = map_to_rank(&full[r.slot], 0);
+          if (issued >= first) {
+            if (r.round > 0 && !mbar_wait(&empty[r.slot], (r.round - 1) & 1, a.err, &s_abort)) {
+              ok = false;
+              break;
+            }
+            expect(t, r.slot);
+            weights(t, kb, st, bar);
+          }
+          rows(t, kb, st, bar);
+          r.next(kStages);
+        }
+      }
+      // the copies in flight land before the pair's shared memory is released
+      if (rank == 0) {
+        for (long long q = issued > kStages ? issued - kStages : 0; q < issued; ++q)
+          mbar_wait_drain(&full[q % kStages], (uint32_t)(q / kStages) & 1, a.err);
+      }
     }
-    __syncthreads();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // ---- MMA issuer
+      Ring r;
+      bool ok = true;
+      Buffers<kDown> buf;
+      Items w(pair, pairs, n_kb, n_tiles, a.max_parts, a.few_rows);
+      while (ok && w.advance()) {
+        const int n = find_tile(s_plan, a.E, mb, w.tile).n;
+        const uint32_t idesc = umma_idesc_bf16(256, n, kDown);
+        buf.take(n);
+        if (buf.used[buf.b] && !mbar_wait(&acce[buf.b], (buf.used[buf.b] - 1) & 1, a.err, &s_abort)) break;
+        if (buf.both && buf.used[1] && !mbar_wait(&acce[1], (buf.used[1] - 1) & 1, a.err, &s_abort)) break;
+        tc_fence_after();
+        const uint32_t d0 = tmem + buf.column(), d1 = d0 + kUpCol;
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          if (!mbar_wait(&full[r.slot], r.round & 1, a.err, &s_abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sb = smem_u32(smem + (size_t)r.slot * C::kStage);
+#pragma unroll
+          for (int k = 0; k < kKB / 16; ++k) {
+            const uint32_t acc = (kb > w.kb0 || k) ? 1u : 0u;
+            const uint64_t br = umma_desc_k(sb + C::kW + 32u * k);
+            if constexpr (kDown) {
+              umma_bf16_pair(d0, umma_desc_mn(sb + 2048u * k, kWBox / 2), br, idesc, acc);
+            } else {
+              umma_bf16_pair(d0, umma_desc_k(sb + 32u * k), br, idesc, acc);
+              umma_bf16_pair(d1, umma_desc_k(sb + kWBox + 32u * k), br, idesc, acc);
+            }
+          }
+          umma_commit_pair(&empty[r.slot]);
+          r.next(kStages);
+        }
+        if (!ok) break;
+        umma_commit_pair(&accf[buf.b]);
+        if (buf.both) umma_commit_pair(&accf[1]);
+        buf.done();
+      }
+      umma_commit_pair(&drain);
+      mbar_wait_drain(&drain, 0, a.err);
+    } else if (lane == 0) {
+      mbar_wait_drain(&drain, 0, a.err);  // the even CTA's last commit has arrived here too
+    }
+  } else {
+    // ---- epilogue: warps 2..9, TMEM lane quarter warp % 4, column half (warp - 2) / 4
+    if (kDown) pdl_wait_prior();  // the parts and counters are the gate/up kernel's until it is done
+    const int quarter = warp & 3, side = (warp - 2) >> 2;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
+    const int out_lane = 32 * quarter + lane;
+    constexpr int kAccs = kDown ? 1 : 2;
+    const size_t part_acc = (size_t)a.part_n / 4 * 128, part_place = kAccs * part_acc * 4;  // float4s, floats
+    Buffers<kDown> buf;
+    Items w(pair, pairs, n_kb, n_tiles, a.max_parts, a.few_rows);
+    while (w.advance()) {
+      const Tile t = find_tile(s_plan, a.E, mb, w.tile);
+      buf.take(t.n);
+      bool got = mbar_wait(&accf[buf.b], buf.used[buf.b] & 1, a.err, &s_abort);
+      if (got && buf.both) got = mbar_wait(&accf[1], buf.used[1] & 1, a.err, &s_abort);
+      // every epilogue warp leaves together (split tiles meet at a named barrier)
+      if (!named_all(1, kEpiWarps * kWarp, got)) break;
+      tc_fence_after();
+      const uint32_t acc = lane_base + buf.column();
+      const int o = t.m * 256 + (int)rank * 128 + out_lane;
+      const int c0 = side * (t.n / 2), c1 = c0 + t.n / 2;
+
+      // 16 columns' results to memory: even lanes keep column k of their own and the next output, odd
+      // lanes column k + 1
+      auto put = [&](int c, float (&g)[16], const float (&u)[16]) {
+        if constexpr (!kDown) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) g[k] = act_fast(g[k], a.act) * u[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+          const float give = (lane & 1) ? g[k] : g[k + 1];
+          const float take = __shfl_xor_sync(0xffffffffu, give, 1);
+          const __nv_bfloat162 v = (lane & 1) ? __floats2bfloat162_rn(take, g[k + 1]) : __floats2bfloat162_rn(g[k], take);
+          const int row = t.row0 + c + k + (lane & 1);
+          if (row < t.row1 && o < a.N)
+            *reinterpret_cast<__nv_bfloat162*>(a.out + (size_t)row * a.N + (o & ~1)) = v;
+        }
+      };
+      const bool whole = w.whole();
+      // this thread's 4-column vectors of the part kept at a place
+      auto part_at = [&](int place) {
+        return reinterpret_cast<float4*>(a.part + (size_t)(place * 2 + (int)rank) * part_place) + out_lane;
+      };
+      float4* mine = whole ? nullptr : part_at(w.my_place());
+      for (int c = c0; c < c1; c += 16) {
+        float g[16], u[16];
+        __syncwarp();
+        tmem_ld16(acc + (uint32_t)c, g);
+        if constexpr (!kDown) tmem_ld16(acc + kUpCol + (uint32_t)c, u);
+        tmem_ld_wait();
+        if (whole) {
+          put(c, g, u);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            __stcg(mine + (size_t)(c / 4 + k) * 128, make_float4(g[4 * k], g[4 * k + 1], g[4 * k + 2], g[4 * k + 3]));
+            if constexpr (!kDown)
+              __stcg(mine + part_acc + (size_t)(c / 4 + k) * 128,
+                     make_float4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]));
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive_cluster(map_to_rank(&acce[buf.b], 0));
+        if (buf.both) mbar_arrive_cluster(map_to_rank(&acce[1], 0));
+      }
+      buf.done();
+      if (whole) continue;
+
+      const int parts = w.parts();
+      uint32_t* ctr = a.ctr + 2 * w.left_tile() + rank;
+      __threadfence();
+      named_sync(2, kEpiWarps * kWarp);
+      if (threadIdx.x == 2 * kWarp) {
+        s_last = atomicAdd(ctr, 1u) + 1u == (uint32_t)parts;
+        if (s_last) *ctr = 0u;
+      }
+      named_sync(2, kEpiWarps * kWarp);
+      if (!s_last) {
+        named_sync(2, kEpiWarps * kWarp);  // s_last is written again by the next part
+        continue;
+      }
+      __threadfence();
+      for (int c = c0; c < c1; c += 16) {
+        float g[16], u[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) g[k] = u[k] = 0.f;
+#pragma unroll 2
+        for (int r = 0; r < parts; ++r) {
+          const float4* from = part_at(w.place(r)) + (size_t)(c / 4) * 128;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 x = __ldcg(from + (size_t)k * 128);
+            g[4 * k] += x.x, g[4 * k + 1] += x.y, g[4 * k + 2] += x.z, g[4 * k + 3] += x.w;
+            if constexpr (!kDown) {
+              const float4 y = __ldcg(from + part_acc + (size_t)k * 128);
+              u[4 * k] += y.x, u[4 * k + 1] += y.y, u[4 * k + 2] += y.z, u[4 * k + 3] += y.w;
+            }
+          }
+        }
+        put(c, g, u);
+      }
+      named_sync(2, kEpiWarps * kWarp);
+    }
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + ty + 16 * i;
-    if (r >= r1) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = c0 + tx + 16 * j;
-      if (c >= p.N) continue;
-      const size_t o = (size_t)r * p.N + c;
-      if (MODE == kLogits)
-        reinterpret_cast<float*>(p.out)[o] = acc0[i][j];
-      else if (MODE == kDown)
-        reinterpret_cast<bf16*>(p.out)[o] = __float2bfloat16_rn(acc0[i][j]);
-      else
-        reinterpret_cast<bf16*>(p.out)[o] = __float2bfloat16_rn(gate_act(acc0[i][j], p.act) * acc1[i][j]);
-    }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // neither CTA's shared memory or TMEM goes while the pair still uses it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
-template <int MODE>
-cudaError_t launch_tiles(const TileArgs& p, cudaStream_t s) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+bool encode(CUtensorMap* tm, const void* base, int rank, const cuuint64_t* dim, const cuuint64_t* stride,
+            const cuuint32_t* box) {
+  TensorMapEncodeFn fn = tensor_map_encoder();
+  const cuuint32_t ones[3] = {1, 1, 1};
+  return fn && fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dim, stride, box, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Weights [E, h, d], boxes of 64 x `high`.
+bool encode_weights(CUtensorMap* tm, const void* base, const MoeFfnArgs& a, cuuint32_t high) {
+  const cuuint64_t dim[3] = {(cuuint64_t)a.d, (cuuint64_t)a.h, (cuuint64_t)a.E};
+  const cuuint64_t stride[2] = {(cuuint64_t)a.d * 2, (cuuint64_t)a.h * a.d * 2};
+  const cuuint32_t box[3] = {64, high, 1};
+  return encode(tm, base, 3, dim, stride, box);
+}
+
+// Rows [rows, width], boxes of 64 x `high`.
+bool encode_rows(CUtensorMap* tm, const void* base, int rows, int width, cuuint32_t high) {
+  const cuuint64_t dim[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+  const cuuint64_t stride[1] = {(cuuint64_t)width * 2};
+  const cuuint32_t box[2] = {64, high};
+  return encode(tm, base, 2, dim, stride, box);
+}
+
+// Pairs of CTAs that fit on the device at once (a static split over more would wait for the first
+// ones to finish), looked up once per device and kernel.
+template <bool kDown>
+cudaError_t resident_pairs(const cudaLaunchConfig_t& cfg, int* out) {
+  static int cached[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || cached[dev] == 0) {
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, pair_kernel<kDown>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (n < 1) return cudaErrorInvalidConfiguration;
+    if (dev < 0 || dev >= 64) {
+      *out = n;
+      return cudaSuccess;
+    }
+    cached[dev] = n;
+  }
+  *out = cached[dev];
+  return cudaSuccess;
+}
+
+template <bool kDown>
+cudaError_t launch_pair(const Args& p, const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& r64,
+                        const CUtensorMap& r16, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(pair_kernel<kDown>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)Cfg<kDown>::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  // an expert's last tile may be ragged: at most one tile more per expert that has rows
-  const int row_tiles = (p.n + kT - 1) / kT + (p.offsets ? (p.E < p.n ? p.E : p.n) : 0);
-  cfg.gridDim = dim3((unsigned)((p.N + kT - 1) / kT), (unsigned)row_tiles);
+  cfg.gridDim = dim3((unsigned)(sm_count() / 2 * 2));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Cfg<kDown>::kSmem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tile_kernel<MODE>, p);
+  cfg.numAttrs = 1;  // the cluster; the dependent launch is no part of the query
+  int pairs = 0;
+  if ((e = resident_pairs<kDown>(cfg, &pairs)) != cudaSuccess) return e;
+  if (pairs > kMoeMaxPairs) pairs = kMoeMaxPairs;
+  // no more pairs than k-blocks there can be: every tile has a row, an expert at most one ragged tile
+  const long long row_tiles = (long long)(p.rows + kMaxN - 1) / kMaxN + (p.E < p.rows ? p.E : p.rows);
+  const long long blocks = row_tiles * ((p.N + 255) / 256) * ((p.K + kKB - 1) / kKB);
+  if (blocks < pairs) pairs = (int)blocks;
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, pair_kernel<kDown>, p, w0, w1, r64, r16);
 }
 
 }  // namespace
 
-cudaError_t launch_moe_logits(const void* x, const void* w, int T, int E, int d, float* logits, cudaStream_t s) {
-  const TileArgs p{static_cast<const bf16*>(x), static_cast<const bf16*>(w), nullptr, nullptr, T, E, d, 1, 0, logits};
-  return launch_tiles<kLogits>(p, s);
-}
-
 cudaError_t launch_moe_ffn(const MoeFfnArgs& a, cudaStream_t s) {
-  const TileArgs gu{static_cast<const bf16*>(a.xs), static_cast<const bf16*>(a.W_gate), static_cast<const bf16*>(a.W_up),
-                    a.offsets, a.rows, a.h, a.d, a.E, a.act, a.v};
-  cudaError_t e = launch_tiles<kGateUp>(gu, s);
+  CUtensorMap tm_g, tm_u, tm_x64, tm_x16, tm_d, tm_v64, tm_v16;
+  if (!encode_weights(&tm_g, a.W_gate, a, 128) || !encode_weights(&tm_u, a.W_up, a, 128) ||
+      !encode_weights(&tm_d, a.W_down_t, a, 64) || !encode_rows(&tm_x64, a.xs, a.rows, a.d, 64) ||
+      !encode_rows(&tm_x16, a.xs, a.rows, a.d, 16) || !encode_rows(&tm_v64, a.v, a.rows, a.h, 64) ||
+      !encode_rows(&tm_v16, a.v, a.rows, a.h, 16))
+    return cudaErrorInvalidValue;
+  const int part_n = moe_part_rows(a.rows), max_parts = part_n <= kMoeFewRows ? kMaxParts : kMaxPartsHigh;
+  const Args gu{a.offsets, a.rows, a.E, a.h, a.d, a.act, static_cast<bf16*>(a.v), a.part, part_n, max_parts,
+                part_n <= kMoeFewRows, a.ctr, a.err};
+  cudaError_t e = launch_pair<false>(gu, tm_g, tm_u, tm_x64, tm_x16, s);
   if (e != cudaSuccess) return e;
-  const TileArgs dn{static_cast<const bf16*>(a.v), static_cast<const bf16*>(a.W_down_t), nullptr,
-                    a.offsets, a.rows, a.d, a.h, a.E, a.act, a.ys};
-  return launch_tiles<kDown>(dn, s);
+  const Args dn{a.offsets, a.rows, a.E, a.d, a.h, a.act, static_cast<bf16*>(a.ys), a.part, part_n, max_parts,
+                part_n <= kMoeFewRows, a.ctr + 2 * kMoeMaxPairs, a.err};
+  return launch_pair<true>(dn, tm_d, tm_d, tm_v64, tm_v16, s);
 }
 
 }  // namespace csffn

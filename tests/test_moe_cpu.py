@@ -119,6 +119,16 @@ def test_ffn_refusals(lib):
     assert need >= lib.csffn_moe_dispatch_workspace_size(8, 4)
 
 
+def test_workspace_for_more_rows_serves_fewer(lib):
+    """The queried sizes never fall as the rows grow."""
+    rows = sorted({r + d for b in range(1, 23) for r in (1 << b, 3 << b >> 1) for d in (-1, 0, 1)} - {0})
+    for L in (moe_layer(h=8), moe_layer(h=1024, E=64)):
+        sizes = [lib.csffn_moe_workspace_size(ctypes.byref(L), r) for r in rows if r <= 1 << 22]
+        assert sizes == sorted(sizes) and sizes[0] > 0
+    sizes = [lib.csffn_moe_dispatch_workspace_size(r, 512) for r in rows if r <= 1 << 22]
+    assert sizes == sorted(sizes) and sizes[0] > 0
+
+
 def test_combine_refusals(lib):
     def f(ys=FAKE, pos=FAKE, w=FAKE, T=4, k=2, rows=8, d=256, out=FAKE, mode=_abi.OUT_F32):
         return lib.csffn_moe_combine(ys, pos, w, T, k, rows, d, out, mode, None)
