@@ -262,48 +262,53 @@ def selftest_timeout(ws: torch.Tensor, spin_limit: int, stream=None) -> None:
 
 # ------------------------------------------------------------------------------ routed FFN, block norm
 
-class _Call:
-    """The tensors of one call: every one contiguous and on one CUDA device, which is made current for
-    the call (kernels launch on the current device), and the stream to launch on: the one given, or
-    that device's current one."""
+# A decode step makes one of these calls every few microseconds, so each argument is checked by one
+# expression and explained only when that fails.
 
-    __slots__ = ("index", "prev")
-
-    def __init__(self, first: torch.Tensor):
-        if not first.is_cuda:
-            raise ValueError("csffn takes CUDA tensors")
-        self.index = first.get_device()
-
-    def ptr(self, t: Optional[torch.Tensor], name: str, shape, *dtypes: torch.dtype):
-        if t is None:
-            return None
-        if t.dtype not in dtypes:
-            raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError("csffn takes contiguous tensors")
-        if t.get_device() != self.index:
-            raise ValueError(f"{name} must be on the device of the call's other tensors (cuda:{self.index})")
-        return t.data_ptr()
-
-    def ws(self, ws: torch.Tensor):
-        return self.ptr(ws, "ws", ws.shape, torch.uint8)
-
-    def run(self, name: str, stream, *args) -> None:
-        s = stream.cuda_stream if stream is not None else torch.cuda.current_stream(self.index).cuda_stream
-        fn = getattr(load(), name)
-        if torch.cuda.current_device() == self.index:
-            status = fn(*args, s)
-        else:
-            with torch.cuda.device(self.index):
-                status = fn(*args, s)
-        if status != _abi.OK:
-            raise CsffnError(status, name)
-
-
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 _CODE = {_BF16: _abi.BF16, _F32: _abi.F32}
+
+
+def _device(t: torch.Tensor) -> int:
+    if not t.is_cuda:
+        raise ValueError("csffn takes CUDA tensors")
+    return t.get_device()
+
+
+def _code(t: torch.Tensor, name: str) -> int:
+    code = _CODE.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, not {t.dtype}")
+    return code
+
+
+def _arg(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype, dev: int):
+    """Pointer of a contiguous tensor of this shape and dtype on device `dev`; None stays None."""
+    if t is None:
+        return None
+    if t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError("csffn takes contiguous tensors")
+    raise ValueError(f"{name} must be on the device of the call's other tensors (cuda:{dev})")
+
+
+def _run(name: str, dev: int, stream, *args) -> None:
+    """Calls the entry point on `stream`, or on the current stream of device `dev`, which is made
+    current for the call (kernels launch on the current device)."""
+    s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+    fn = getattr(load(), name)
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, s)
+    if status != _abi.OK:
+        raise CsffnError(status, name)
 
 
 def _matrix(t: torch.Tensor, name: str):
@@ -325,9 +330,9 @@ class MoELayer:
     def __post_init__(self):
         if self.w_gate.dim() != 3:
             raise ValueError("w_gate must be [n_experts, h, d]")
-        call = _Call(self.w_gate)
+        dev = _device(self.w_gate)
         E, h, d = self.w_gate.shape
-        ptrs = [call.ptr(w, n, self.w_gate.shape, _BF16)
+        ptrs = [_arg(w, n, self.w_gate.shape, _BF16, dev)
                 for w, n in ((self.w_gate, "w_gate"), (self.w_up, "w_up"), (self.w_down_t, "w_down_t"))]
         self.c = _abi.MoELayer(d, h, E, self.act, *ptrs)
 
@@ -377,9 +382,9 @@ def new_moe_dispatch_workspace(max_rows: int, n_experts: int, device="cuda") -> 
 def moe_logits(x: torch.Tensor, w_router: torch.Tensor, logits: torch.Tensor, stream=None) -> None:
     """logits [T, E] fp32 = x [T, d] . w_router [E, d]^T (bf16 operands, fp32 sums)."""
     (T, d), (E, _) = _matrix(x, "x"), _matrix(w_router, "w_router")
-    c = _Call(x)
-    c.run("csffn_moe_logits", stream, c.ptr(x, "x", (T, d), _BF16), c.ptr(w_router, "w_router", (E, d), _BF16), T, E, d,
-          c.ptr(logits, "logits", (T, E), _F32))
+    dev = _device(x)
+    _run("csffn_moe_logits", dev, stream, _arg(x, "x", (T, d), _BF16, dev), _arg(w_router, "w_router", (E, d), _BF16, dev),
+         T, E, d, _arg(logits, "logits", (T, E), _F32, dev))
 
 
 def moe_route(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -387,10 +392,11 @@ def moe_route(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, bi
     """The k = ids.shape[1] experts of every token, by logits [T, E] (plus bias [E] for the choice
     alone), and their weights; see csffn_moe_route."""
     (T, E), (_, k) = _matrix(logits, "logits"), _matrix(ids, "ids")
-    c = _Call(logits)
-    c.run("csffn_moe_route", stream, c.ptr(logits, "logits", (T, E), _F32, _BF16), _CODE[logits.dtype],
-          c.ptr(bias, "bias", (E,), _F32), T, E, k, score, int(renormalize), scale, c.ptr(ids, "ids", (T, k), _I32),
-          c.ptr(weights, "weights", (T, k), _F32))
+    dev = _device(logits)
+    code = _code(logits, "logits")
+    _run("csffn_moe_route", dev, stream, _arg(logits, "logits", (T, E), logits.dtype, dev), code,
+         _arg(bias, "bias", (E,), _F32, dev), T, E, k, score, renormalize, scale, _arg(ids, "ids", (T, k), _I32, dev),
+         _arg(weights, "weights", (T, k), _F32, dev))
 
 
 def moe_dispatch(x: torch.Tensor, ids: torch.Tensor, offsets: torch.Tensor, order: torch.Tensor, pos: torch.Tensor,
@@ -398,12 +404,12 @@ def moe_dispatch(x: torch.Tensor, ids: torch.Tensor, offsets: torch.Tensor, orde
     """Sorts the token slots by expert and gathers the tokens' rows into xs [T * k, d]; the number of
     experts is offsets.shape[0] - 1.  See csffn_moe_dispatch."""
     (T, d), (_, k) = _matrix(x, "x"), _matrix(ids, "ids")
-    E = offsets.numel() - 1
-    c = _Call(x)
-    c.run("csffn_moe_dispatch", stream, c.ptr(x, "x", (T, d), _BF16, _F32), _CODE[x.dtype],
-          c.ptr(ids, "ids", (T, k), _I32), T, k, E, d, c.ptr(offsets, "offsets", (E + 1,), _I32),
-          c.ptr(order, "order", (T * k,), _I32), c.ptr(pos, "pos", (T, k), _I32), c.ptr(xs, "xs", (T * k, d), x.dtype),
-          c.ws(ws), ws.numel())
+    E, n = offsets.numel() - 1, ws.numel()
+    dev = _device(x)
+    code = _code(x, "x")
+    _run("csffn_moe_dispatch", dev, stream, _arg(x, "x", (T, d), x.dtype, dev), code, _arg(ids, "ids", (T, k), _I32, dev),
+         T, k, E, d, _arg(offsets, "offsets", (E + 1,), _I32, dev), _arg(order, "order", (T * k,), _I32, dev),
+         _arg(pos, "pos", (T, k), _I32, dev), _arg(xs, "xs", (T * k, d), x.dtype, dev), _arg(ws, "ws", (n,), _U8, dev), n)
 
 
 def moe_ffn_forward(layer: MoELayer, xs: torch.Tensor, offsets: torch.Tensor, ys: torch.Tensor, ws: torch.Tensor,
@@ -411,12 +417,12 @@ def moe_ffn_forward(layer: MoELayer, xs: torch.Tensor, offsets: torch.Tensor, ys
     """The experts' gated FFNs on the sorted rows xs [rows, d] -> ys [rows, d] (bf16); see
     csffn_moe_ffn_forward.  ws: new_moe_workspace(layer, rows or more)."""
     rows, _ = _matrix(xs, "xs")
-    c = _Call(xs)
-    if layer.w_gate.get_device() != c.index:
+    dev, n = _device(xs), ws.numel()
+    if layer.w_gate.get_device() != dev:
         raise ValueError("the layer must be on the device of the rows")
-    c.run("csffn_moe_ffn_forward", stream, layer.ref(), c.ptr(xs, "xs", (rows, layer.d), _BF16),
-          c.ptr(offsets, "offsets", (layer.n_experts + 1,), _I32), rows, c.ptr(ys, "ys", (rows, layer.d), _BF16),
-          c.ws(ws), ws.numel())
+    _run("csffn_moe_ffn_forward", dev, stream, layer.ref(), _arg(xs, "xs", (rows, layer.d), _BF16, dev),
+         _arg(offsets, "offsets", (layer.n_experts + 1,), _I32, dev), rows, _arg(ys, "ys", (rows, layer.d), _BF16, dev),
+         _arg(ws, "ws", (n,), _U8, dev), n)
 
 
 def moe_combine(ys: torch.Tensor, pos: torch.Tensor, weights: Optional[torch.Tensor], out: torch.Tensor,
@@ -425,10 +431,10 @@ def moe_combine(ys: torch.Tensor, pos: torch.Tensor, weights: Optional[torch.Ten
     (rows, d), (T, k) = _matrix(ys, "ys"), _matrix(pos, "pos")
     if out_mode is None:
         out_mode = _abi.OUT_BF16 if out.dtype == _BF16 else _abi.OUT_F32
-    c = _Call(out)
-    c.run("csffn_moe_combine", stream, c.ptr(ys, "ys", (rows, d), _BF16), c.ptr(pos, "pos", (T, k), _I32),
-          c.ptr(weights, "weights", (T, k), _F32), T, k, rows, d,
-          c.ptr(out, "out", (T, d), _BF16 if out_mode == _abi.OUT_BF16 else _F32), out_mode)
+    dev = _device(out)
+    _run("csffn_moe_combine", dev, stream, _arg(ys, "ys", (rows, d), _BF16, dev), _arg(pos, "pos", (T, k), _I32, dev),
+         _arg(weights, "weights", (T, k), _F32, dev), T, k, rows, d,
+         _arg(out, "out", (T, d), _BF16 if out_mode == _abi.OUT_BF16 else _F32, dev), out_mode)
 
 
 def block_norm(h: torch.Tensor, y: Optional[torch.Tensor], h_out: Optional[torch.Tensor],
@@ -438,13 +444,16 @@ def block_norm(h: torch.Tensor, y: Optional[torch.Tensor], h_out: Optional[torch
     """h_out = res_scale * h + out_scale * gate * rms(y) * g_post, xn = rms(h_out) * g_pre; see
     csffn_block_norm.  gate: [d] (per channel) or [T, d] (per token)."""
     T, d = _matrix(h, "h")
+    dev = _device(h)
+    rows, row = (T, d), (d,)
     per_token = gate is not None and gate.dim() == 2
-    c = _Call(h)
-    c.run("csffn_block_norm", stream, c.ptr(h, "h", (T, d), _F32), c.ptr(y, "y", (T, d), _BF16, _F32),
-          _abi.BF16 if y is None else _CODE[y.dtype], c.ptr(g_post, "g_post", (d,), _F32),
-          c.ptr(gate, "gate", (T, d) if per_token else (d,), _F32), T if per_token else 1,
-          c.ptr(g_pre, "g_pre", (d,), _F32), res_scale, out_scale, eps, T, d, c.ptr(h_out, "h_out", (T, d), _F32),
-          c.ptr(xn, "xn", (T, d), _BF16, _F32), _abi.BF16 if xn is None else _CODE[xn.dtype])
+    ycode = _abi.BF16 if y is None else _code(y, "y")
+    xcode = _abi.BF16 if xn is None else _code(xn, "xn")
+    _run("csffn_block_norm", dev, stream, _arg(h, "h", rows, _F32, dev),
+         None if y is None else _arg(y, "y", rows, y.dtype, dev), ycode, _arg(g_post, "g_post", row, _F32, dev),
+         _arg(gate, "gate", rows if per_token else row, _F32, dev), T if per_token else 1,
+         _arg(g_pre, "g_pre", row, _F32, dev), res_scale, out_scale, eps, T, d, _arg(h_out, "h_out", rows, _F32, dev),
+         None if xn is None else _arg(xn, "xn", rows, xn.dtype, dev), xcode)
 
 
 # ------------------------------------------------------------------------------ buffers

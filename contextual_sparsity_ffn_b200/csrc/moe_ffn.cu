@@ -210,17 +210,18 @@ struct Items {
 template <bool kDown>
 struct Buffers {
   int turn = 0;
-  uint32_t used[2] = {0, 0};
+  uint32_t used0 = 0, used1 = 0;
   int b;      // first buffer of the item
   bool both;  // it takes both
+  __device__ uint32_t used() const { return b ? used1 : used0; }
   __device__ void take(int n) {
     both = !kDown && n > 128;
     b = both ? 0 : turn;
     if (!both) turn ^= 1;
   }
   __device__ void done() {
-    ++used[b];
-    if (both) ++used[1];
+    if (b == 0) ++used0;
+    if (b == 1 || both) ++used1;
   }
   __device__ uint32_t column() const { return kDown ? 256u * b : 128u * b; }
 };
@@ -369,8 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = find_tile(s_plan, a.E, mb, w.tile).n;
         const uint32_t idesc = umma_idesc_bf16(256, n, kDown);
         buf.take(n);
-        if (buf.used[buf.b] && !mbar_wait(&acce[buf.b], (buf.used[buf.b] - 1) & 1, a.err, &s_abort)) break;
-        if (buf.both && buf.used[1] && !mbar_wait(&acce[1], (buf.used[1] - 1) & 1, a.err, &s_abort)) break;
+        if (buf.used() && !mbar_wait(&acce[buf.b], (buf.used() - 1) & 1, a.err, &s_abort)) break;
+        if (buf.both && buf.used1 && !mbar_wait(&acce[1], (buf.used1 - 1) & 1, a.err, &s_abort)) break;
         tc_fence_after();
         const uint32_t d0 = tmem + buf.column(), d1 = d0 + kUpCol;
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
@@ -417,8 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (w.advance()) {
       const Tile t = find_tile(s_plan, a.E, mb, w.tile);
       buf.take(t.n);
-      bool got = mbar_wait(&accf[buf.b], buf.used[buf.b] & 1, a.err, &s_abort);
-      if (got && buf.both) got = mbar_wait(&accf[1], buf.used[1] & 1, a.err, &s_abort);
+      bool got = mbar_wait(&accf[buf.b], buf.used() & 1, a.err, &s_abort);
+      if (got && buf.both) got = mbar_wait(&accf[1], buf.used1 & 1, a.err, &s_abort);
       // every epilogue warp leaves together (split tiles meet at a named barrier)
       if (!named_all(1, kEpiWarps * kWarp, got)) break;
       tc_fence_after();

@@ -213,7 +213,6 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* t
       "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-
 // Bounded wait that ignores the CTA's abort flag: for draining copies or MMAs still in flight before
 // the CTA's shared memory or TMEM is released.  Gives up after a second and records the timeout.
 __device__ __forceinline__ void mbar_wait_drain(uint64_t* bar, uint32_t parity, uint32_t* err) {
