@@ -19,7 +19,7 @@ MoeWs moe_ws_layout(int rows, int E, int h) {
   // the most chunks any call of up to `rows` slots has
   const int chunks = (rows + kMoeChunk - 1) / kMoeChunk;
   const size_t hist = sizeof(int32_t) * (size_t)(chunks < kMoeMaxChunks ? chunks : kMoeMaxChunks) * E;
-  const size_t v = sizeof(bf16) * (size_t)rows * h;
+  const size_t v = sizeof(bf16) * moe_v_rows(rows, E) * h;
   o += align_up(hist > v ? hist : v, 256);
   L.part = o;
   if (h > 0) o += sizeof(float) * moe_part_floats(rows);

@@ -207,14 +207,28 @@ struct MoeWs {          // workspace of csffn_moe_dispatch and csffn_moe_ffn_for
   size_t err;           // uint32 error word, where WsLayout has it (csffn_check_status)
   size_t hist;          // dispatch: int32 [chunks][E] expert counts per chunk of slots
   size_t ctr;           // ffn: uint32 [2 kernels][kMoeMaxPairs][2] split tiles' counters, zero between calls
-  size_t v;             // ffn: bf16 [rows][h]
+  size_t v;             // ffn: bf16 [moe_v_rows(rows, E)][h]
   size_t part;          // ffn: fp32 split tiles' parts, moe_part_floats(rows)
   size_t total;
 };
 constexpr int kMoeTileRows = 256;  // most rows of one expert per tile
+constexpr int kMoeLowTile = 32;    // the same where experts have few rows
 constexpr int kMoeMaxPairs = 80;   // most CTA pairs at work
-constexpr int kMoeFewRows = 64;    // tiles this low may be parts of two tiles per pair
+// Whether a call's experts have few rows each, by what the host knows of them.
+inline int moe_low_rows(int E) { return 4 * E > 64 ? 4 * E : 64; }
+inline bool moe_low(int rows, int E) { return rows <= moe_low_rows(E); }
+// Rows of v kept for a call of up to `rows` rows: calls of few rows keep a high and a low part.
+inline size_t moe_v_rows(int rows, int E) {
+  const int low = 2 * (rows < moe_low_rows(E) ? rows : moe_low_rows(E));
+  return (size_t)(rows > low ? rows : low);
+}
 inline int moe_part_rows(int rows) { return rows >= kMoeTileRows ? kMoeTileRows : (rows + 31) / 32 * 32; }
+// Split tiles' parts, [places][2 CTAs][2 accumulators][rows of a tile][128]: a place per pair, or two
+// with few rows per tile.
+inline size_t moe_part_floats(int rows) {
+  const int tall = kMoeMaxPairs * moe_part_rows(rows), low = 2 * kMoeMaxPairs * kMoeLowTile;
+  return (size_t)(tall > low ? tall : low) * 2 * 2 * 128;
+}
 constexpr int kMoeChunk = 1024;     // least slots per counting chunk
 constexpr int kMoeMaxChunks = 256;  // most chunks: each placing CTA adds up all chunks' counts
 inline int moe_chunk_slots(int rows) {
@@ -222,11 +236,6 @@ inline int moe_chunk_slots(int rows) {
   return per <= kMoeChunk ? kMoeChunk : (per + kMoeChunk - 1) / kMoeChunk * kMoeChunk;
 }
 inline int moe_chunks(int rows) { return (rows + moe_chunk_slots(rows) - 1) / moe_chunk_slots(rows); }
-inline size_t moe_part_floats(int rows) {  // [places][2 CTAs][2 accumulators][rows of a tile][128]
-  const int n = moe_part_rows(rows);  // a workspace for more rows also serves fewer
-  const int all = n <= 2 * kMoeFewRows ? 2 * kMoeMaxPairs * (n < kMoeFewRows ? n : kMoeFewRows) : kMoeMaxPairs * n;
-  return (size_t)all * 2 * 2 * 128;
-}
 MoeWs moe_ws_layout(int rows, int E, int h);  // h == 0: the dispatch's part alone
 
 cudaError_t launch_moe_logits(const void* x, const void* w, int T, int E, int d, float* logits, cudaStream_t s);

@@ -9,9 +9,14 @@
 // is whatever the router made it: N is any multiple of 32 up to 256 chosen per tile, so a ragged
 // expert wastes at most 31 rows of multiplication and none of the weight traffic.
 //
+// Few rows per expert (kLow) is the weights' stream and little else: tiles of 32 rows, so that a stage
+// is nearly all weights.  v is kept as a bf16 high part and a bf16 low part there (v - high), the two halves of the down product's N side: about 16
+// bits of v reach the product at no cost in time.  With many rows, where the products are the time,
+// v is rounded once to bf16.
+//
 // Work split: whole tiles go round the pairs as long as there is one for every pair.  The R tiles
 // left over (all of them in a decode step) would leave pairs idle, so they are cut along the
-// contraction.  Up to half as many tiles as pairs: each into S = pairs / R parts (at most kMaxParts),
+// contraction where that pays.  Up to half as many tiles as pairs: each into S = pairs / R parts (at most kMaxParts),
 // one part per pair.  More, with few rows: the tiles' k-blocks, in order, form one run that is
 // divided evenly among the pairs (a pair holds parts of at most two tiles).  A pair with a part
 // stores its fp32 accumulators in the workspace and counts up the tile's counter; the last one adds
@@ -29,9 +34,9 @@
 // drained while the next tile accumulates: 256 TMEM columns each (down), or 128 columns each of gate
 // and of up; a gate/up tile of more than 128 rows takes both.
 //
-// Warp roles (320 threads): warp 0 issues the copies, warp 1 owns TMEM and (even CTA) issues the
-// MMAs, warps 2-9 run the epilogue: TMEM lane = output, column = row, two warps per lane quarter, each
-// half of the columns.  Neighbouring lanes exchange one value of each column pair so that a lane
+// Warp roles: warp 0 issues the copies, warp 1 owns TMEM and (even CTA) issues the MMAs, the other
+// 8 run the epilogue: TMEM lane = output, column = row, two warps per lane quarter, each half of the
+// columns.  Neighbouring lanes exchange one value of each column pair so that a lane
 // stores two adjacent outputs (4 bytes).
 //
 // Row bounds come from the device: `offsets` is clamped to 0 .. rows and to ascending order when it is
@@ -45,31 +50,37 @@
 namespace csffn {
 namespace {
 
-constexpr int kThreads = 320;
-constexpr int kEpiWarps = 8;
-constexpr int kMaxN = kMoeTileRows;                   // rows per tile
-constexpr int kKB = 64;                               // contraction elements per stage
-constexpr uint32_t kWBox = 128 * kKB * 2;             // one CTA's 128 outputs x 64: 16 KB
-constexpr uint32_t kRowsMax = (kMaxN / 2) * kKB * 2;  // one CTA's half of the rows: 16 KB
-constexpr int kMaxParts = 8, kMaxPartsHigh = 4;       // parts of a tile of at most / more than 64 rows
-constexpr uint32_t kUpCol = 256;                      // TMEM column of the up accumulator / second buffer
+constexpr int kKB = 64;                 // contraction elements per stage
+constexpr uint32_t kRowBytes = kKB * 2;  // one row of a stage's tile
+constexpr uint32_t kWBox = 128 * kRowBytes;  // one CTA's 128 outputs x 64: 16 KB
+constexpr int kMaxParts = 8, kMaxPartsTall = 4;     // parts of a tile
+constexpr int kMinSaved = 16, kMinSavedTall = 24;  // k-blocks
 
-template <bool kDown>
+template <bool kDown, bool kLow>
 struct Cfg {
-  static constexpr uint32_t kW = kDown ? kWBox : 2 * kWBox;
-  static constexpr uint32_t kStage = kW + kRowsMax;
-  static constexpr int kStages = kDown ? 6 : 4;
+  static constexpr int kTileRows = kLow ? kMoeLowTile : kMoeTileRows;  // most rows per tile
+  static constexpr int kParts = kDown && kLow ? 2 : 1;                 // high and low part of v
+  static constexpr int kAccs = kDown ? 1 : 2;                          // gate and up
+  static constexpr int kEpiWarps = 8;
+  static constexpr int kSides = kEpiWarps / 4;         // shares of a tile's columns
+  static constexpr int kThreads = (2 + kEpiWarps) * kWarp;
+  static constexpr uint32_t kW = kAccs * kWBox;
+  static constexpr uint32_t kStage = kW + (uint32_t)(kParts * kTileRows / 2) * kRowBytes;
+  static constexpr int kStages = kLow ? (kDown ? 10 : 6) : (kDown ? 6 : 4);
   static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
+  // Accumulator columns: two buffers; up is kUp columns behind gate.  A gate/up tile of more than 128
+  // rows takes both buffers.
+  static constexpr uint32_t kBuffer = kLow ? 32u * kParts : kDown ? 256u : 128u;
+  static constexpr uint32_t kUp = 2 * kBuffer;
+  static constexpr uint32_t kColumns = kLow ? 128 : 512;
 };
 
 struct Args {
   const int32_t* offsets;
   int rows, E, N, K, act;  // N outputs per expert, K contraction
-  bf16* out;               // [rows, N]
+  bf16* out;               // [rows, N]; gate/up with few rows: [2][rows, N], high and low parts
   float* part;             // [places][2 CTAs][accumulators][part_n / 4][128][4] split tiles' parts
   int part_n;              // most rows of a tile of this call
-  int max_parts;
-  bool few_rows;
   uint32_t* ctr;           // [pairs][2]: parts done of the split tiles
   uint32_t* err;
 };
@@ -82,6 +93,7 @@ struct Plan {
 };
 
 // By one warp, from the raw offsets in p->lo: each lane takes a few consecutive entries.
+template <int kTileRows>
 __device__ void make_plan(const Args& a, Plan* p) {
   const int lane = threadIdx.x & 31, per = (a.E + kWarp) / kWarp;  // E + 1 entries
   const int e0 = min(lane * per, a.E + 1), e1 = min(e0 + per, a.E + 1);
@@ -102,7 +114,7 @@ __device__ void make_plan(const Args& a, Plan* p) {
   for (int e = e0; e < e1; ++e) {
     const int v = max(p->lo[e], before);
     p->lo[e] = v;
-    if (e > 0) tiles += (v - prev + kMaxN - 1) / kMaxN;
+    if (e > 0) tiles += (v - prev + kTileRows - 1) / kTileRows;
     p->tp[e] = tiles;
     prev = v;
   }
@@ -152,12 +164,15 @@ struct Items {
   int next;                              // next whole tile
   int it, it1;                           // this pair's k-blocks of the run
   int tile, kb0, kb1;                    // the current item
-  __device__ Items(int pair_, int pairs_, int n_kb_, int n_tiles, int max_parts, bool few_rows)
+  __device__ Items(int pair_, int pairs_, int n_kb_, int n_tiles, bool low)
       : pair(pair_), pairs(pairs_), n_kb(n_kb_) {
     n_whole = n_tiles / pairs * pairs;
     left = n_tiles - n_whole;
-    split = left ? min(min(pairs / left, max_parts), n_kb) : 1;
-    if (split == 1 && left > 0 && few_rows && n_kb >= 4) split = 0;
+    // A part costs its accumulators' way through L2 and about 4 us at the end, as much as 16 k-blocks
+    // of a low tile or 20 of a tall one: cut only where that many k-blocks less are to be done.
+    split = left ? min(min(pairs / left, low ? kMaxParts : kMaxPartsTall), n_kb) : 1;
+    if (n_kb - n_kb / split < (low ? kMinSaved : kMinSavedTall)) split = 1;
+    if (low && left && pairs / left == 1 && n_kb - (int)((long long)n_kb * left / pairs) >= kMinSaved) split = 0;
     next = pair;
     it = split == 0 ? run_start(pair) : 0;
     it1 = split == 0 ? run_start(pair + 1) : 0;
@@ -207,7 +222,7 @@ struct Items {
 
 // Which accumulator buffers an item takes, and how often each was taken before: every role counts the
 // same items, so they agree on the barriers' phases.
-template <bool kDown>
+template <bool kDown, bool kLow>
 struct Buffers {
   int turn = 0;
   uint32_t used0 = 0, used1 = 0;
@@ -215,7 +230,7 @@ struct Buffers {
   bool both;  // it takes both
   __device__ uint32_t used() const { return b ? used1 : used0; }
   __device__ void take(int n) {
-    both = !kDown && n > 128;
+    both = !kDown && !kLow && n > 128;
     b = both ? 0 : turn;
     if (!both) turn ^= 1;
   }
@@ -223,7 +238,7 @@ struct Buffers {
     if (b == 0) ++used0;
     if (b == 1 || both) ++used1;
   }
-  __device__ uint32_t column() const { return kDown ? 256u * b : 128u * b; }
+  __device__ uint32_t column() const { return Cfg<kDown, kLow>::kBuffer * b; }
 };
 
 struct Ring {
@@ -243,12 +258,12 @@ __device__ __forceinline__ float act_fast(float z, int act) {
   return act == CSFFN_ACT_SILU ? __fdividef(z, 1.0f + __expf(-z)) : fmaxf(z, 0.0f);
 }
 
-template <bool kDown>
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool kDown, bool kLow>
+__global__ void __launch_bounds__(Cfg<kDown, kLow>::kThreads, 1)
     pair_kernel(const Args a, const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ CUtensorMap tm_w1,
-                const __grid_constant__ CUtensorMap tm_r64, const __grid_constant__ CUtensorMap tm_r16) {
-  using C = Cfg<kDown>;
-  constexpr int kStages = C::kStages;
+                const __grid_constant__ CUtensorMap tm_high, const __grid_constant__ CUtensorMap tm_r16) {
+  using C = Cfg<kDown, kLow>;
+  constexpr int kStages = C::kStages, kEpiWarps = C::kEpiWarps, kChunk = 16;
   extern __shared__ __align__(1024) unsigned char moe_raw[];
   __shared__ __align__(8) uint64_t full[kStages], empty[kStages], accf[2], acce[2], drain;
   __shared__ uint32_t s_tmem;
@@ -265,8 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     tma_prefetch_map(&tm_w0);
     if (!kDown) tma_prefetch_map(&tm_w1);
-    tma_prefetch_map(&tm_r64);
-    tma_prefetch_map(&tm_r16);
+    tma_prefetch_map(&tm_high);
+    if (!kLow) tma_prefetch_map(&tm_r16);
     s_abort = 0;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
@@ -280,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc_pair(&s_tmem, 512);
+    tmem_alloc_pair(&s_tmem, C::kColumns);
     tmem_relinquish_pair();
   }
   tc_fence_before();
@@ -293,9 +308,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // before the down kernel's wait, v after it.
   if (!kDown) pdl_wait_prior();
   pdl_trigger();
-  for (int e = threadIdx.x; e <= a.E; e += kThreads) s_plan.lo[e] = __ldcg(a.offsets + e);
+  for (int e = threadIdx.x; e <= a.E; e += C::kThreads) s_plan.lo[e] = __ldcg(a.offsets + e);
   __syncthreads();
-  if (warp == 0) make_plan(a, &s_plan);
+  if (warp == 0) make_plan<C::kTileRows>(a, &s_plan);
   __syncthreads();
   const int n_tiles = s_plan.tp[a.E] * mb;
 
@@ -315,16 +330,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d_pair(st + kWBox, &tm_w1, kb * kKB, out0, t.e, bar);
         }
       };
+      // bytes of a tile's rows in one CTA: half of them, or all rows of one part of v
+      auto row_bytes = [&](const Tile& t) { return (uint32_t)(kLow ? C::kParts * C::kTileRows / 2 : t.n / 2) * kRowBytes; };
       auto rows = [&](const Tile& t, int kb, unsigned char* st, uint32_t bar) {
-        const int half = t.n / 2, row0 = t.row0 + (int)rank * half;
-        int n = 0;
-        for (; n + 64 <= half; n += 64) tma_load_2d_pair(st + C::kW + n * (kKB * 2), &tm_r64, kb * kKB, row0 + n, bar);
-        for (; n < half; n += 16) tma_load_2d_pair(st + C::kW + n * (kKB * 2), &tm_r16, kb * kKB, row0 + n, bar);
+        if constexpr (kLow) {
+          const int row = kDown ? t.row0 + (int)rank * a.rows : t.row0 + (int)rank * (C::kTileRows / 2);
+          tma_load_2d_pair(st + C::kW, &tm_high, kb * kKB, row, bar);
+        } else {
+          const int half = t.n / 2, row0 = t.row0 + (int)rank * half;
+          int n = 0;
+          for (; n + 64 <= half; n += 64) tma_load_2d_pair(st + C::kW + n * kRowBytes, &tm_high, kb * kKB, row0 + n, bar);
+          for (; n < half; n += 16) tma_load_2d_pair(st + C::kW + n * kRowBytes, &tm_r16, kb * kKB, row0 + n, bar);
+        }
       };
       auto expect = [&](const Tile& t, int slot) {
-        if (rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * (C::kW + (uint32_t)(t.n / 2) * (kKB * 2)));
+        if (rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * (C::kW + row_bytes(t)));
       };
-      Items w(pair, pairs, n_kb, n_tiles, a.max_parts, a.few_rows);
+      Items w(pair, pairs, n_kb, n_tiles, kLow);
       bool more = w.advance();
       int first = 0;  // stages of the first item whose weights went out before the wait
       if (kDown && more) {
@@ -364,16 +386,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- MMA issuer
       Ring r;
       bool ok = true;
-      Buffers<kDown> buf;
-      Items w(pair, pairs, n_kb, n_tiles, a.max_parts, a.few_rows);
+      Buffers<kDown, kLow> buf;
+      Items w(pair, pairs, n_kb, n_tiles, kLow);
       while (ok && w.advance()) {
         const int n = find_tile(s_plan, a.E, mb, w.tile).n;
-        const uint32_t idesc = umma_idesc_bf16(256, n, kDown);
+        const uint32_t idesc = umma_idesc_bf16(256, kLow ? C::kParts * C::kTileRows : n, kDown);
         buf.take(n);
         if (buf.used() && !mbar_wait(&acce[buf.b], (buf.used() - 1) & 1, a.err, &s_abort)) break;
         if (buf.both && buf.used1 && !mbar_wait(&acce[1], (buf.used1 - 1) & 1, a.err, &s_abort)) break;
         tc_fence_after();
-        const uint32_t d0 = tmem + buf.column(), d1 = d0 + kUpCol;
+        const uint32_t d0 = tmem + buf.column(), d1 = d0 + C::kUp;
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
           if (!mbar_wait(&full[r.slot], r.round & 1, a.err, &s_abort)) {
             ok = false;
@@ -406,15 +428,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_drain(&drain, 0, a.err);  // the even CTA's last commit has arrived here too
     }
   } else {
-    // ---- epilogue: warps 2..9, TMEM lane quarter warp % 4, column half (warp - 2) / 4
+    // ---- epilogue: warps 2..9, TMEM lane quarter warp % 4, share (warp - 2) / 4 of the columns
     if (kDown) pdl_wait_prior();  // the parts and counters are the gate/up kernel's until it is done
     const int quarter = warp & 3, side = (warp - 2) >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
     const int out_lane = 32 * quarter + lane;
-    constexpr int kAccs = kDown ? 1 : 2;
-    const size_t part_acc = (size_t)a.part_n / 4 * 128, part_place = kAccs * part_acc * 4;  // float4s, floats
-    Buffers<kDown> buf;
-    Items w(pair, pairs, n_kb, n_tiles, a.max_parts, a.few_rows);
+    const size_t part_acc = (size_t)a.part_n / 4 * 128, part_place = C::kAccs * part_acc * 4;  // float4s, floats
+    Buffers<kDown, kLow> buf;
+    Items w(pair, pairs, n_kb, n_tiles, kLow);
     while (w.advance()) {
       const Tile t = find_tile(s_plan, a.E, mb, w.tile);
       buf.take(t.n);
@@ -425,23 +446,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t acc = lane_base + buf.column();
       const int o = t.m * 256 + (int)rank * 128 + out_lane;
-      const int c0 = side * (t.n / 2), c1 = c0 + t.n / 2;
+      const int width = kLow ? C::kTileRows / C::kSides : t.n / C::kSides, c0 = side * width, c1 = c0 + width;
 
-      // 16 columns' results to memory: even lanes keep column k of their own and the next output, odd
+      // a chunk of columns' results to memory: even lanes keep column k of their own and the next output, odd
       // lanes column k + 1
-      auto put = [&](int c, float (&g)[16], const float (&u)[16]) {
+      auto put = [&](int c, float (&g)[kChunk], const float (&u)[kChunk]) {
         if constexpr (!kDown) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) g[k] = act_fast(g[k], a.act) * u[k];
+          for (int k = 0; k < kChunk; ++k) g[k] = act_fast(g[k], a.act) * u[k];
         }
 #pragma unroll
-        for (int k = 0; k < 16; k += 2) {
+        for (int k = 0; k < kChunk; k += 2) {
           const float give = (lane & 1) ? g[k] : g[k + 1];
           const float take = __shfl_xor_sync(0xffffffffu, give, 1);
-          const __nv_bfloat162 v = (lane & 1) ? __floats2bfloat162_rn(take, g[k + 1]) : __floats2bfloat162_rn(g[k], take);
+          const float first = (lane & 1) ? take : g[k], second = (lane & 1) ? g[k + 1] : take;
+          const __nv_bfloat162 v = __floats2bfloat162_rn(first, second);
           const int row = t.row0 + c + k + (lane & 1);
-          if (row < t.row1 && o < a.N)
-            *reinterpret_cast<__nv_bfloat162*>(a.out + (size_t)row * a.N + (o & ~1)) = v;
+          if (row < t.row1 && o < a.N) {
+            __nv_bfloat162* at = reinterpret_cast<__nv_bfloat162*>(a.out + (size_t)row * a.N + (o & ~1));
+            *at = v;
+            if constexpr (kLow && !kDown)
+              at[(size_t)a.rows * a.N / 2] =
+                  __floats2bfloat162_rn(first - __low2float(v), second - __high2float(v));
+          }
         }
       };
       const bool whole = w.whole();
@@ -450,17 +477,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         return reinterpret_cast<float4*>(a.part + (size_t)(place * 2 + (int)rank) * part_place) + out_lane;
       };
       float4* mine = whole ? nullptr : part_at(w.my_place());
-      for (int c = c0; c < c1; c += 16) {
-        float g[16], u[16];
+      for (int c = c0; c < c1; c += kChunk) {
+        float g[kChunk], u[kChunk];
         __syncwarp();
         tmem_ld16(acc + (uint32_t)c, g);
-        if constexpr (!kDown) tmem_ld16(acc + kUpCol + (uint32_t)c, u);
+        if constexpr (C::kAccs == 2) tmem_ld16(acc + C::kUp + (uint32_t)c, u);
+        if constexpr (C::kParts == 2) tmem_ld16(acc + 32u + (uint32_t)c, u);
         tmem_ld_wait();
+        if constexpr (C::kParts == 2) {  // the low part of v's share
+#pragma unroll
+          for (int k = 0; k < kChunk; ++k) g[k] += u[k];
+        }
         if (whole) {
           put(c, g, u);
         } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < kChunk / 4; ++k) {
             __stcg(mine + (size_t)(c / 4 + k) * 128, make_float4(g[4 * k], g[4 * k + 1], g[4 * k + 2], g[4 * k + 3]));
             if constexpr (!kDown)
               __stcg(mine + part_acc + (size_t)(c / 4 + k) * 128,
@@ -491,15 +523,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       __threadfence();
-      for (int c = c0; c < c1; c += 16) {
-        float g[16], u[16];
+      for (int c = c0; c < c1; c += kChunk) {
+        float g[kChunk], u[kChunk];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) g[k] = u[k] = 0.f;
+        for (int k = 0; k < kChunk; ++k) g[k] = u[k] = 0.f;
 #pragma unroll 2
         for (int r = 0; r < parts; ++r) {
           const float4* from = part_at(w.place(r)) + (size_t)(c / 4) * 128;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < kChunk / 4; ++k) {
             const float4 x = __ldcg(from + (size_t)k * 128);
             g[4 * k] += x.x, g[4 * k + 1] += x.y, g[4 * k + 2] += x.z, g[4 * k + 3] += x.w;
             if constexpr (!kDown) {
@@ -518,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync_all();  // neither CTA's shared memory or TMEM goes while the pair still uses it
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, 512);
+    tmem_dealloc_pair(tmem, C::kColumns);
   }
 }
 
@@ -547,34 +579,32 @@ bool encode_rows(CUtensorMap* tm, const void* base, int rows, int width, cuuint3
   return encode(tm, base, 2, dim, stride, box);
 }
 
-// Pairs of CTAs that fit on the device at once (a static split over more would wait for the first
-// ones to finish), looked up once per device and kernel.
-template <bool kDown>
+// Pairs of CTAs to launch: as many as fit on the device at once (a static split over more would
+// wait for the first ones to finish), looked up once per device and kernel.
+template <bool kDown, bool kLow>
 cudaError_t resident_pairs(const cudaLaunchConfig_t& cfg, int* out) {
   static int cached[64] = {0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || cached[dev] == 0) {
-    int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, pair_kernel<kDown>, &cfg);
+  int n = dev >= 0 && dev < 64 ? cached[dev] : 0;
+  if (n == 0) {
+    e = cudaOccupancyMaxActiveClusters(&n, pair_kernel<kDown, kLow>, &cfg);
     if (e != cudaSuccess) return e;
+    if (n > kMoeMaxPairs) n = kMoeMaxPairs;
     if (n < 1) return cudaErrorInvalidConfiguration;
-    if (dev < 0 || dev >= 64) {
-      *out = n;
-      return cudaSuccess;
-    }
-    cached[dev] = n;
+    if (dev >= 0 && dev < 64) cached[dev] = n;
   }
-  *out = cached[dev];
+  *out = n;
   return cudaSuccess;
 }
 
-template <bool kDown>
-cudaError_t launch_pair(const Args& p, const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& r64,
+template <bool kDown, bool kLow>
+cudaError_t launch_pair(const Args& p, const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& high,
                         const CUtensorMap& r16, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(pair_kernel<kDown>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)Cfg<kDown>::kSmem);
+  using C = Cfg<kDown, kLow>;
+  cudaError_t e = cudaFuncSetAttribute(pair_kernel<kDown, kLow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)C::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -585,40 +615,50 @@ cudaError_t launch_pair(const Args& p, const CUtensorMap& w0, const CUtensorMap&
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(sm_count() / 2 * 2));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Cfg<kDown>::kSmem;
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;  // the cluster; the dependent launch is no part of the query
   int pairs = 0;
-  if ((e = resident_pairs<kDown>(cfg, &pairs)) != cudaSuccess) return e;
-  if (pairs > kMoeMaxPairs) pairs = kMoeMaxPairs;
+  if ((e = resident_pairs<kDown, kLow>(cfg, &pairs)) != cudaSuccess) return e;
   // no more pairs than k-blocks there can be: every tile has a row, an expert at most one ragged tile
-  const long long row_tiles = (long long)(p.rows + kMaxN - 1) / kMaxN + (p.E < p.rows ? p.E : p.rows);
+  const long long row_tiles = (long long)(p.rows + C::kTileRows - 1) / C::kTileRows + (p.E < p.rows ? p.E : p.rows);
   const long long blocks = row_tiles * ((p.N + 255) / 256) * ((p.K + kKB - 1) / kKB);
   if (blocks < pairs) pairs = (int)blocks;
   cfg.gridDim = dim3((unsigned)(2 * pairs));
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, pair_kernel<kDown>, p, w0, w1, r64, r16);
+  return cudaLaunchKernelEx(&cfg, pair_kernel<kDown, kLow>, p, w0, w1, high, r16);
+}
+
+template <bool kLow>
+cudaError_t launch_ffn(const MoeFfnArgs& a, cudaStream_t s) {
+  // boxes of the rows: all that a CTA takes of a tile (few rows), or 64 and 16 at a time
+  const cuuint32_t high_x = kLow ? kMoeLowTile / 2 : 64, high_v = kLow ? kMoeLowTile : 64;
+  CUtensorMap tm_g, tm_u, tm_x, tm_x16, tm_d, tm_v, tm_v16;
+  if (!encode_weights(&tm_g, a.W_gate, a, 128) || !encode_weights(&tm_u, a.W_up, a, 128) ||
+      !encode_weights(&tm_d, a.W_down_t, a, 64) || !encode_rows(&tm_x, a.xs, a.rows, a.d, high_x) ||
+      !encode_rows(&tm_v, a.v, kLow ? 2 * a.rows : a.rows, a.h, high_v))
+    return cudaErrorInvalidValue;
+  if (kLow) {
+    tm_x16 = tm_x;
+    tm_v16 = tm_v;
+  } else if (!encode_rows(&tm_x16, a.xs, a.rows, a.d, 16) || !encode_rows(&tm_v16, a.v, a.rows, a.h, 16)) {
+    return cudaErrorInvalidValue;
+  }
+  const int part_n = kLow ? kMoeLowTile : moe_part_rows(a.rows);
+  const Args gu{a.offsets, a.rows, a.E, a.h, a.d, a.act, static_cast<bf16*>(a.v), a.part, part_n, a.ctr, a.err};
+  cudaError_t e = launch_pair<false, kLow>(gu, tm_g, tm_u, tm_x, tm_x16, s);
+  if (e != cudaSuccess) return e;
+  const Args dn{a.offsets, a.rows, a.E,    a.d,    a.h, a.act, static_cast<bf16*>(a.ys), a.part,
+                part_n,    a.ctr + 2 * kMoeMaxPairs, a.err};
+  return launch_pair<true, kLow>(dn, tm_d, tm_d, tm_v, tm_v16, s);
 }
 
 }  // namespace
 
 cudaError_t launch_moe_ffn(const MoeFfnArgs& a, cudaStream_t s) {
-  CUtensorMap tm_g, tm_u, tm_x64, tm_x16, tm_d, tm_v64, tm_v16;
-  if (!encode_weights(&tm_g, a.W_gate, a, 128) || !encode_weights(&tm_u, a.W_up, a, 128) ||
-      !encode_weights(&tm_d, a.W_down_t, a, 64) || !encode_rows(&tm_x64, a.xs, a.rows, a.d, 64) ||
-      !encode_rows(&tm_x16, a.xs, a.rows, a.d, 16) || !encode_rows(&tm_v64, a.v, a.rows, a.h, 64) ||
-      !encode_rows(&tm_v16, a.v, a.rows, a.h, 16))
-    return cudaErrorInvalidValue;
-  const int part_n = moe_part_rows(a.rows), max_parts = part_n <= kMoeFewRows ? kMaxParts : kMaxPartsHigh;
-  const Args gu{a.offsets, a.rows, a.E, a.h, a.d, a.act, static_cast<bf16*>(a.v), a.part, part_n, max_parts,
-                part_n <= kMoeFewRows, a.ctr, a.err};
-  cudaError_t e = launch_pair<false>(gu, tm_g, tm_u, tm_x64, tm_x16, s);
-  if (e != cudaSuccess) return e;
-  const Args dn{a.offsets, a.rows, a.E, a.d, a.h, a.act, static_cast<bf16*>(a.ys), a.part, part_n, max_parts,
-                part_n <= kMoeFewRows, a.ctr + 2 * kMoeMaxPairs, a.err};
-  return launch_pair<true>(dn, tm_d, tm_d, tm_v64, tm_v16, s);
+  return moe_low(a.rows, a.E) ? launch_ffn<true>(a, s) : launch_ffn<false>(a, s);
 }
 
 }  // namespace csffn

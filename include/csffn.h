@@ -385,7 +385,8 @@ size_t csffn_moe_workspace_size(const csffn_moe_layer* layer, int max_rows);
  *   xs: bf16 [rows, d]; offsets: int32 [n_experts + 1] on the device, ascending, as
  *   csffn_moe_dispatch writes it (values are clamped to 0 .. rows and to ascending order); ys: bf16
  *   [rows, d]; rows at and behind offsets[n_experts] are left as they were.  xs and ys must not
- *   overlap.  Sums are fp32; v is rounded once to bf16 for the down projection. */
+ *   overlap.  Sums are fp32; for the down projection v is a bf16 high part plus a bf16 low part
+ *   where the experts have few rows (rows <= max(64, 4 n_experts)), else rounded once to bf16. */
 csffn_status csffn_moe_ffn_forward(const csffn_moe_layer* layer, const void* xs, const int32_t* offsets, int rows,
                                    void* ys, void* ws, size_t ws_bytes, void* stream);
 
