@@ -38,31 +38,42 @@ cudaError_t launch_chained(void (*kern)(P...), int grid, int block, size_t smem,
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// The expert of slot s, or E for slots that are dropped (padding, or past the end).
-__device__ __forceinline__ int slot_expert(const DispatchArgs& a, int s, int end) {
-  if (s >= end) return a.E;
-  const int e = a.ids[s];
-  return e >= 0 && e < a.E ? e : a.E;
+constexpr int kRounds = kMoeChunk / kSortThreads;  // rounds of 32 slots per warp and batch
+
+// This warp's slots of chunk [c0, c1) from round r0 on: lane's slot in round r is *first + 32 r, and its
+// expert ex[r], or E for slots that are dropped (padding, or past the chunk).  All loads go out at
+// once.
+__device__ __forceinline__ void load_slots(const DispatchArgs& a, int c0, int c1, int warp, int lane, int r0,
+                                           int (&ex)[kRounds], int* first) {
+  const int per = (c1 - c0 + kSortThreads - 1) / kSortThreads * kWarp;  // slots of a warp
+  const int lo = c0 + warp * per, hi = min(lo + per, c1);
+  *first = lo + r0 * kWarp + lane;
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int s = *first + r * kWarp;
+    ex[r] = s < hi ? __ldcg(a.ids + s) : -1;
+  }
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) ex[r] = ex[r] >= 0 && ex[r] < a.E ? ex[r] : a.E;
+}
+// Rounds of a chunk: whole batches.
+__device__ __forceinline__ int chunk_rounds(int c0, int c1) {
+  return ((c1 - c0 + kSortThreads - 1) / kSortThreads + kRounds - 1) / kRounds * kRounds;
 }
 
-// Slots [lo, hi) of this warp within chunk [c0, c1): contiguous, 32 at a time.
-__device__ __forceinline__ void warp_span(int c0, int c1, int warp, int* lo, int* hi) {
-  const int per = ((c1 - c0 + kSortWarps - 1) / kSortWarps + kWarp - 1) / kWarp * kWarp;
-  *lo = min(c0 + warp * per, c1);
-  *hi = min(*lo + per, c1);
-}
-
-// whist[w][e] = slots of expert e in warp w's span.
-__device__ void count_warps(const DispatchArgs& a, int c0, int c1, int* whist, int warp, int lane) {
+// whist[w][e] = slots of expert e in warp w's share of the chunk.  `ex` holds the first batch.
+__device__ void count_warps(const DispatchArgs& a, int c0, int c1, int* whist, int warp, int lane, int (&ex)[kRounds]) {
   for (int i = threadIdx.x; i < kSortWarps * a.E; i += kSortThreads) whist[i] = 0;
   __syncthreads();
-  int lo, hi;
-  warp_span(c0, c1, warp, &lo, &hi);
-  for (int s0 = lo; s0 < hi; s0 += kWarp) {
-    const int e = slot_expert(a, s0 + lane, hi);
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
-    if (e < a.E && lane == __ffs(same) - 1) whist[warp * a.E + e] += __popc(same);
-    __syncwarp();
+  for (int r0 = 0; r0 < chunk_rounds(c0, c1); r0 += kRounds) {
+    int first;
+    if (r0 > 0) load_slots(a, c0, c1, warp, lane, r0, ex, &first);
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      const uint32_t same = __match_any_sync(0xffffffffu, ex[r]);
+      if (ex[r] < a.E && lane == __ffs(same) - 1) whist[warp * a.E + ex[r]] += __popc(same);
+      __syncwarp();
+    }
   }
   __syncthreads();
 }
@@ -72,7 +83,9 @@ __global__ void __launch_bounds__(kSortThreads) count_kernel(const DispatchArgs 
   pdl_trigger();
   pdl_wait_prior();
   const int R = a.T * a.k, c0 = blockIdx.x * chunk, c1 = min(R, c0 + chunk);
-  count_warps(a, c0, c1, sort_smem, threadIdx.x >> 5, threadIdx.x & 31);
+  int ex[kRounds], first;
+  load_slots(a, c0, c1, threadIdx.x >> 5, threadIdx.x & 31, 0, ex, &first);
+  count_warps(a, c0, c1, sort_smem, threadIdx.x >> 5, threadIdx.x & 31, ex);
   for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
     int n = 0;
 #pragma unroll
@@ -105,12 +118,12 @@ __device__ int scan_experts(int* tot, int E, int* s_sum) {
 }
 
 // Places this chunk's slots: calls put(slot, position) for every slot, position -1 for a dropped
-// one.  `first[e]`: position of the chunk's first slot of expert e.  whist: as count_warps left it.
+// one.  `start[e]`: position of the chunk's first slot of expert e.  whist: as count_warps left it.
 template <typename Put>
-__device__ void place_chunk(const DispatchArgs& a, int c0, int c1, int* whist, const int* first, int warp, int lane,
-                            Put put) {
+__device__ void place_chunk(const DispatchArgs& a, int c0, int c1, int* whist, const int* start, int warp, int lane,
+                            int (&ex)[kRounds], Put put) {
   for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
-    int n = first[e];
+    int n = start[e];
 #pragma unroll
     for (int w = 0; w < kSortWarps; ++w) {
       const int c = whist[w * a.E + e];
@@ -119,17 +132,23 @@ __device__ void place_chunk(const DispatchArgs& a, int c0, int c1, int* whist, c
     }
   }
   __syncthreads();
-  int lo, hi;
-  warp_span(c0, c1, warp, &lo, &hi);
-  for (int s0 = lo; s0 < hi; s0 += kWarp) {
-    const int s = s0 + lane, e = slot_expert(a, s, hi);
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
-    const int rank = __popc(same & ((1u << lane) - 1u));
-    const int base = e < a.E ? whist[warp * a.E + e] : 0;
-    __syncwarp();
-    if (e < a.E && rank == 0) whist[warp * a.E + e] = base + __popc(same);
-    __syncwarp();
-    if (s < hi) put(s, e < a.E ? base + rank : -1);
+  const int per = (c1 - c0 + kSortThreads - 1) / kSortThreads * kWarp;
+  const int hi = min(c0 + (warp + 1) * per, c1);
+  const int rounds = chunk_rounds(c0, c1);
+  for (int r0 = 0; r0 < rounds; r0 += kRounds) {
+    int first = c0 + warp * per + lane;
+    if (rounds > kRounds) load_slots(a, c0, c1, warp, lane, r0, ex, &first);
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      const int s = first + r * kWarp, e = ex[r];
+      const uint32_t same = __match_any_sync(0xffffffffu, e);
+      const int rank = __popc(same & ((1u << lane) - 1u));
+      const int base = e < a.E ? whist[warp * a.E + e] : 0;
+      __syncwarp();
+      if (e < a.E && rank == 0) whist[warp * a.E + e] = base + __popc(same);
+      __syncwarp();
+      if (s < hi) put(s, e < a.E ? base + rank : -1);
+    }
   }
 }
 
@@ -143,14 +162,30 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const DispatchArgs 
   pdl_wait_prior();
   const int R = a.T * a.k, c0 = blockIdx.x * chunk, c1 = min(R, c0 + chunk);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
-    int all = 0, mine = 0;
-    for (int c = 0; c < n_chunks; ++c) {
-      if (c == (int)blockIdx.x) mine = all;
-      all += __ldcg(a.hist + (size_t)c * a.E + e);
+  int ex[kRounds], first;
+  load_slots(a, c0, c1, warp, lane, 0, ex, &first);
+  for (int e = threadIdx.x; e < 2 * a.E; e += kSortThreads) tot[e] = 0;  // and `before`
+  __syncthreads();
+  // The chunks' counts, added by groups of threads with a share of the chunks each (integers: the
+  // order of the additions does not matter).
+  const int wide = min(a.E, kSortThreads), groups = kSortThreads / wide, g = threadIdx.x / wide;
+  if (g < groups) {
+    const int lo = g * n_chunks / groups, hi = (g + 1) * n_chunks / groups;
+    for (int e = threadIdx.x % wide; e < a.E; e += wide) {
+      int all = 0, mine = 0;
+      for (int q = lo; q < hi; q += 8) {
+        int n[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) n[u] = q + u < hi ? __ldcg(a.hist + (size_t)(q + u) * a.E + e) : 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          all += n[u];
+          if (q + u < (int)blockIdx.x) mine += n[u];
+        }
+      }
+      atomicAdd(&tot[e], all);
+      atomicAdd(&before[e], mine);
     }
-    tot[e] = all;
-    before[e] = mine;
   }
   const int kept = scan_experts(tot, a.E, &s_sum);
   if (blockIdx.x == 0) {
@@ -158,8 +193,8 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const DispatchArgs 
     if (threadIdx.x == 0) a.offsets[a.E] = kept;
   }
   for (int e = threadIdx.x; e < a.E; e += kSortThreads) before[e] += tot[e];
-  count_warps(a, c0, c1, whist, warp, lane);
-  place_chunk(a, c0, c1, whist, before, warp, lane, [&](int s, int p) {
+  count_warps(a, c0, c1, whist, warp, lane, ex);
+  place_chunk(a, c0, c1, whist, before, warp, lane, ex, [&](int s, int p) {
     a.pos[s] = p;
     if (p >= 0) a.order[p] = s;
   });
@@ -202,7 +237,9 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_small_kernel(const Disp
   pdl_trigger();
   pdl_wait_prior();
   const int R = a.T * a.k, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  count_warps(a, 0, R, whist, warp, lane);
+  int ex[kRounds], first;
+  load_slots(a, 0, R, warp, lane, 0, ex, &first);
+  count_warps(a, 0, R, whist, warp, lane, ex);
   for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
     int n = 0;
 #pragma unroll
@@ -211,7 +248,7 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_small_kernel(const Disp
   }
   const int kept = scan_experts(tot, a.E, &s_sum);
   const bool lead = blockIdx.x == 0;
-  place_chunk(a, 0, R, whist, tot, warp, lane, [&](int s, int p) {
+  place_chunk(a, 0, R, whist, tot, warp, lane, ex, [&](int s, int p) {
     s_pos[s] = p;
     if (lead) {
       a.pos[s] = p;
