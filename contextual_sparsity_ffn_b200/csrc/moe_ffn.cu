@@ -9,17 +9,22 @@
 // is whatever the router made it: N is any multiple of 32 up to 256 chosen per tile, so a ragged
 // expert wastes at most 31 rows of multiplication and none of the weight traffic.
 //
+// The down kernel's tiles are 512 columns wide where there are enough of them (kWide): two blocks of
+// 256 that share the rows, as gate and up do.  What bounds these tiles with many rows is the operands'
+// way from L2 to the SMs: 64 bytes a cycle and SM for 256 x 256 at the tensor cores' full rate, 48 for
+// 512 x 256.
+//
 // Few rows per expert (kLow) is the weights' stream and little else: tiles of 32 rows, so that a stage
-// is nearly all weights.  v is kept as a bf16 high part and a bf16 low part there (v - high), the two halves of the down product's N side: about 16
-// bits of v reach the product at no cost in time.  With many rows, where the products are the time,
-// v is rounded once to bf16.
+// is nearly all weights.  v is kept as a bf16 high part and a bf16 low part there (v - high), the two
+// halves of the down product's N side: about 16 bits of v reach the product at no cost in time.  With
+// many rows, where the products are the time, v is rounded once to bf16.
 //
 // Work split: whole tiles go round the pairs as long as there is one for every pair.  The R tiles
 // left over (all of them in a decode step) would leave pairs idle, so they are cut along the
-// contraction where that pays.  Up to half as many tiles as pairs: each into S = pairs / R parts (at most kMaxParts),
-// one part per pair.  More, with few rows: the tiles' k-blocks, in order, form one run that is
-// divided evenly among the pairs (a pair holds parts of at most two tiles).  A pair with a part
-// stores its fp32 accumulators in the workspace and counts up the tile's counter; the last one adds
+// contraction where that pays.  Up to half as many tiles as pairs: each into S = pairs / R parts (at
+// most kMaxParts), one part per pair.  More, with few rows: the tiles' k-blocks, in order, form one
+// run that is divided evenly among the pairs (a pair holds parts of at most two tiles).  A pair with a
+// part stores its fp32 accumulators in the workspace and counts up the tile's counter; the last one adds
 // the parts in their order (the same bits whoever is last), writes the tile and clears the counter.
 // No pair waits for another.
 //
@@ -29,15 +34,16 @@
 //
 // Operands come by TMA tensor copies with the 128-byte swizzle, 64 contraction elements per stage:
 // W_gate and W_up 128 x 64 each (gate/up, K-major) or W_down^T as two boxes of 64 columns x 64
-// neurons (down, MN-major), and half the tile's rows in each CTA.  All copies of a stage complete on
-// one barrier of the pair's even CTA, whose MMA warp issues for both.  Accumulators: two buffers, one
-// drained while the next tile accumulates: 256 TMEM columns each (down), or 128 columns each of gate
-// and of up; a gate/up tile of more than 128 rows takes both.
+// neurons per block (down, MN-major), and half the tile's rows in each CTA.  All copies of a stage
+// complete on one barrier of the pair's even CTA, whose MMA warp issues for both.  Accumulators: two buffers, one
+// drained while the next tile accumulates: 256 TMEM columns each, or 128 columns of each of two
+// accumulators (gate and up, the blocks of a wide tile); a tile of more than 128 rows with two
+// accumulators takes both buffers.
 //
 // Warp roles: warp 0 issues the copies, warp 1 owns TMEM and (even CTA) issues the MMAs, the other
 // 8 run the epilogue: TMEM lane = output, column = row, two warps per lane quarter, each half of the
-// columns.  Neighbouring lanes exchange one value of each column pair so that a lane
-// stores two adjacent outputs (4 bytes).
+// columns.  Neighbouring lanes exchange one value of each column pair so that a lane stores two
+// adjacent outputs (4 bytes).
 //
 // Row bounds come from the device: `offsets` is clamped to 0 .. rows and to ascending order when it is
 // read, so no offsets can lead an access outside the buffers.  Every wait is bounded (one second)
@@ -50,27 +56,28 @@
 namespace csffn {
 namespace {
 
-constexpr int kKB = 64;                 // contraction elements per stage
-constexpr uint32_t kRowBytes = kKB * 2;  // one row of a stage's tile
-constexpr uint32_t kWBox = 128 * kRowBytes;  // one CTA's 128 outputs x 64: 16 KB
-constexpr int kMaxParts = 8, kMaxPartsTall = 4;     // parts of a tile
+constexpr int kKB = 64;                            // contraction elements per stage
+constexpr uint32_t kRowBytes = kKB * 2;            // one row of a stage's tile
+constexpr uint32_t kWBox = 128 * kRowBytes;        // one CTA's 128 outputs x 64: 16 KB
+constexpr int kMaxParts = 8, kMaxPartsTall = 4;    // parts of a tile
 constexpr int kMinSaved = 16, kMinSavedTall = 24;  // k-blocks
 
-template <bool kDown, bool kLow>
+template <bool kDown, bool kLow, bool kWide>
 struct Cfg {
+  static constexpr int kTileOut = kWide ? 512 : 256;                   // outputs per tile
   static constexpr int kTileRows = kLow ? kMoeLowTile : kMoeTileRows;  // most rows per tile
   static constexpr int kParts = kDown && kLow ? 2 : 1;                 // high and low part of v
-  static constexpr int kAccs = kDown ? 1 : 2;                          // gate and up
+  static constexpr int kAccs = kDown && !kWide ? 1 : 2;                // gate and up, or two blocks of 256 columns
   static constexpr int kEpiWarps = 8;
   static constexpr int kSides = kEpiWarps / 4;         // shares of a tile's columns
   static constexpr int kThreads = (2 + kEpiWarps) * kWarp;
   static constexpr uint32_t kW = kAccs * kWBox;
   static constexpr uint32_t kStage = kW + (uint32_t)(kParts * kTileRows / 2) * kRowBytes;
-  static constexpr int kStages = kLow ? (kDown ? 10 : 6) : (kDown ? 6 : 4);
+  static constexpr int kStages = kLow ? (kDown ? 10 : 6) : (kAccs == 1 ? 6 : 4);
   static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
-  // Accumulator columns: two buffers; up is kUp columns behind gate.  A gate/up tile of more than 128
-  // rows takes both buffers.
-  static constexpr uint32_t kBuffer = kLow ? 32u * kParts : kDown ? 256u : 128u;
+  // Accumulator columns: two buffers; the second accumulator is kUp columns behind the first.  With two
+  // accumulators a tile of more than 128 rows takes both buffers.
+  static constexpr uint32_t kBuffer = kLow ? 32u * kParts : kAccs == 1 ? 256u : 128u;
   static constexpr uint32_t kUp = 2 * kBuffer;
   static constexpr uint32_t kColumns = kLow ? 128 : 512;
 };
@@ -222,7 +229,7 @@ struct Items {
 
 // Which accumulator buffers an item takes, and how often each was taken before: every role counts the
 // same items, so they agree on the barriers' phases.
-template <bool kDown, bool kLow>
+template <bool kDown, bool kLow, bool kWide>
 struct Buffers {
   int turn = 0;
   uint32_t used0 = 0, used1 = 0;
@@ -230,7 +237,7 @@ struct Buffers {
   bool both;  // it takes both
   __device__ uint32_t used() const { return b ? used1 : used0; }
   __device__ void take(int n) {
-    both = !kDown && !kLow && n > 128;
+    both = Cfg<kDown, kLow, kWide>::kAccs == 2 && !kLow && n > 128;
     b = both ? 0 : turn;
     if (!both) turn ^= 1;
   }
@@ -238,7 +245,7 @@ struct Buffers {
     if (b == 0) ++used0;
     if (b == 1 || both) ++used1;
   }
-  __device__ uint32_t column() const { return Cfg<kDown, kLow>::kBuffer * b; }
+  __device__ uint32_t column() const { return Cfg<kDown, kLow, kWide>::kBuffer * b; }
 };
 
 struct Ring {
@@ -258,11 +265,11 @@ __device__ __forceinline__ float act_fast(float z, int act) {
   return act == CSFFN_ACT_SILU ? __fdividef(z, 1.0f + __expf(-z)) : fmaxf(z, 0.0f);
 }
 
-template <bool kDown, bool kLow>
-__global__ void __launch_bounds__(Cfg<kDown, kLow>::kThreads, 1)
+template <bool kDown, bool kLow, bool kWide>
+__global__ void __launch_bounds__(Cfg<kDown, kLow, kWide>::kThreads, 1)
     pair_kernel(const Args a, const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ CUtensorMap tm_w1,
                 const __grid_constant__ CUtensorMap tm_high, const __grid_constant__ CUtensorMap tm_r16) {
-  using C = Cfg<kDown, kLow>;
+  using C = Cfg<kDown, kLow, kWide>;
   constexpr int kStages = C::kStages, kEpiWarps = C::kEpiWarps, kChunk = 16;
   extern __shared__ __align__(1024) unsigned char moe_raw[];
   __shared__ __align__(8) uint64_t full[kStages], empty[kStages], accf[2], acce[2], drain;
@@ -275,7 +282,7 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int mb = (a.N + 255) / 256, n_kb = (a.K + kKB - 1) / kKB;
+  const int mb = (a.N + C::kTileOut - 1) / C::kTileOut, n_kb = (a.K + kKB - 1) / kKB;
 
   if (threadIdx.x == 0) {
     tma_prefetch_map(&tm_w0);
@@ -321,10 +328,13 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow>::kThreads, 1)
       long long issued = 0;
       bool ok = true;
       auto weights = [&](const Tile& t, int kb, unsigned char* st, uint32_t bar) {
-        const int out0 = t.m * 256 + (int)rank * 128;
+        const int out0 = t.m * C::kTileOut + (int)rank * 128;
         if constexpr (kDown) {
-          tma_load_3d_pair(st, &tm_w0, out0, kb * kKB, t.e, bar);
-          tma_load_3d_pair(st + kWBox / 2, &tm_w0, out0 + 64, kb * kKB, t.e, bar);
+#pragma unroll
+          for (int b = 0; b < C::kAccs; ++b) {
+            tma_load_3d_pair(st + b * kWBox, &tm_w0, out0 + 256 * b, kb * kKB, t.e, bar);
+            tma_load_3d_pair(st + b * kWBox + kWBox / 2, &tm_w0, out0 + 256 * b + 64, kb * kKB, t.e, bar);
+          }
         } else {
           tma_load_3d_pair(st, &tm_w0, kb * kKB, out0, t.e, bar);
           tma_load_3d_pair(st + kWBox, &tm_w1, kb * kKB, out0, t.e, bar);
@@ -386,7 +396,7 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow>::kThreads, 1)
       // ---- MMA issuer
       Ring r;
       bool ok = true;
-      Buffers<kDown, kLow> buf;
+      Buffers<kDown, kLow, kWide> buf;
       Items w(pair, pairs, n_kb, n_tiles, kLow);
       while (ok && w.advance()) {
         const int n = find_tile(s_plan, a.E, mb, w.tile).n;
@@ -409,6 +419,7 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow>::kThreads, 1)
             const uint64_t br = umma_desc_k(sb + C::kW + 32u * k);
             if constexpr (kDown) {
               umma_bf16_pair(d0, umma_desc_mn(sb + 2048u * k, kWBox / 2), br, idesc, acc);
+              if constexpr (kWide) umma_bf16_pair(d1, umma_desc_mn(sb + kWBox + 2048u * k, kWBox / 2), br, idesc, acc);
             } else {
               umma_bf16_pair(d0, umma_desc_k(sb + 32u * k), br, idesc, acc);
               umma_bf16_pair(d1, umma_desc_k(sb + kWBox + 32u * k), br, idesc, acc);
@@ -434,7 +445,7 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow>::kThreads, 1)
     const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
     const int out_lane = 32 * quarter + lane;
     const size_t part_acc = (size_t)a.part_n / 4 * 128, part_place = C::kAccs * part_acc * 4;  // float4s, floats
-    Buffers<kDown, kLow> buf;
+    Buffers<kDown, kLow, kWide> buf;
     Items w(pair, pairs, n_kb, n_tiles, kLow);
     while (w.advance()) {
       const Tile t = find_tile(s_plan, a.E, mb, w.tile);
@@ -445,16 +456,12 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow>::kThreads, 1)
       if (!named_all(1, kEpiWarps * kWarp, got)) break;
       tc_fence_after();
       const uint32_t acc = lane_base + buf.column();
-      const int o = t.m * 256 + (int)rank * 128 + out_lane;
+      const int o = t.m * C::kTileOut + (int)rank * 128 + out_lane;
       const int width = kLow ? C::kTileRows / C::kSides : t.n / C::kSides, c0 = side * width, c1 = c0 + width;
 
       // a chunk of columns' results to memory: even lanes keep column k of their own and the next output, odd
       // lanes column k + 1
-      auto put = [&](int c, float (&g)[kChunk], const float (&u)[kChunk]) {
-        if constexpr (!kDown) {
-#pragma unroll
-          for (int k = 0; k < kChunk; ++k) g[k] = act_fast(g[k], a.act) * u[k];
-        }
+      auto put16 = [&](int c, const float (&g)[kChunk], int out) {
 #pragma unroll
         for (int k = 0; k < kChunk; k += 2) {
           const float give = (lane & 1) ? g[k] : g[k + 1];
@@ -462,14 +469,22 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow>::kThreads, 1)
           const float first = (lane & 1) ? take : g[k], second = (lane & 1) ? g[k + 1] : take;
           const __nv_bfloat162 v = __floats2bfloat162_rn(first, second);
           const int row = t.row0 + c + k + (lane & 1);
-          if (row < t.row1 && o < a.N) {
-            __nv_bfloat162* at = reinterpret_cast<__nv_bfloat162*>(a.out + (size_t)row * a.N + (o & ~1));
+          if (row < t.row1 && out < a.N) {
+            __nv_bfloat162* at = reinterpret_cast<__nv_bfloat162*>(a.out + (size_t)row * a.N + (out & ~1));
             *at = v;
             if constexpr (kLow && !kDown)
               at[(size_t)a.rows * a.N / 2] =
                   __floats2bfloat162_rn(first - __low2float(v), second - __high2float(v));
           }
         }
+      };
+      auto put = [&](int c, float (&g)[kChunk], const float (&u)[kChunk]) {
+        if constexpr (!kDown) {
+#pragma unroll
+          for (int k = 0; k < kChunk; ++k) g[k] = act_fast(g[k], a.act) * u[k];
+        }
+        put16(c, g, o);
+        if constexpr (kWide) put16(c, u, o + 256);
       };
       const bool whole = w.whole();
       // this thread's 4-column vectors of the part kept at a place
@@ -494,7 +509,7 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow>::kThreads, 1)
 #pragma unroll
           for (int k = 0; k < kChunk / 4; ++k) {
             __stcg(mine + (size_t)(c / 4 + k) * 128, make_float4(g[4 * k], g[4 * k + 1], g[4 * k + 2], g[4 * k + 3]));
-            if constexpr (!kDown)
+            if constexpr (C::kAccs == 2)
               __stcg(mine + part_acc + (size_t)(c / 4 + k) * 128,
                      make_float4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]));
           }
@@ -534,7 +549,7 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow>::kThreads, 1)
           for (int k = 0; k < kChunk / 4; ++k) {
             const float4 x = __ldcg(from + (size_t)k * 128);
             g[4 * k] += x.x, g[4 * k + 1] += x.y, g[4 * k + 2] += x.z, g[4 * k + 3] += x.w;
-            if constexpr (!kDown) {
+            if constexpr (C::kAccs == 2) {
               const float4 y = __ldcg(from + part_acc + (size_t)k * 128);
               u[4 * k] += y.x, u[4 * k + 1] += y.y, u[4 * k + 2] += y.z, u[4 * k + 3] += y.w;
             }
@@ -581,7 +596,7 @@ bool encode_rows(CUtensorMap* tm, const void* base, int rows, int width, cuuint3
 
 // Pairs of CTAs to launch: as many as fit on the device at once (a static split over more would
 // wait for the first ones to finish), looked up once per device and kernel.
-template <bool kDown, bool kLow>
+template <bool kDown, bool kLow, bool kWide>
 cudaError_t resident_pairs(const cudaLaunchConfig_t& cfg, int* out) {
   static int cached[64] = {0};
   int dev = 0;
@@ -589,7 +604,7 @@ cudaError_t resident_pairs(const cudaLaunchConfig_t& cfg, int* out) {
   if (e != cudaSuccess) return e;
   int n = dev >= 0 && dev < 64 ? cached[dev] : 0;
   if (n == 0) {
-    e = cudaOccupancyMaxActiveClusters(&n, pair_kernel<kDown, kLow>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, pair_kernel<kDown, kLow, kWide>, &cfg);
     if (e != cudaSuccess) return e;
     if (n > kMoeMaxPairs) n = kMoeMaxPairs;
     if (n < 1) return cudaErrorInvalidConfiguration;
@@ -599,11 +614,11 @@ cudaError_t resident_pairs(const cudaLaunchConfig_t& cfg, int* out) {
   return cudaSuccess;
 }
 
-template <bool kDown, bool kLow>
+template <bool kDown, bool kLow, bool kWide>
 cudaError_t launch_pair(const Args& p, const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& high,
                         const CUtensorMap& r16, cudaStream_t s) {
-  using C = Cfg<kDown, kLow>;
-  cudaError_t e = cudaFuncSetAttribute(pair_kernel<kDown, kLow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  using C = Cfg<kDown, kLow, kWide>;
+  cudaError_t e = cudaFuncSetAttribute(pair_kernel<kDown, kLow, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)C::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
@@ -621,14 +636,14 @@ cudaError_t launch_pair(const Args& p, const CUtensorMap& w0, const CUtensorMap&
   cfg.attrs = attr;
   cfg.numAttrs = 1;  // the cluster; the dependent launch is no part of the query
   int pairs = 0;
-  if ((e = resident_pairs<kDown, kLow>(cfg, &pairs)) != cudaSuccess) return e;
+  if ((e = resident_pairs<kDown, kLow, kWide>(cfg, &pairs)) != cudaSuccess) return e;
   // no more pairs than k-blocks there can be: every tile has a row, an expert at most one ragged tile
   const long long row_tiles = (long long)(p.rows + C::kTileRows - 1) / C::kTileRows + (p.E < p.rows ? p.E : p.rows);
-  const long long blocks = row_tiles * ((p.N + 255) / 256) * ((p.K + kKB - 1) / kKB);
+  const long long blocks = row_tiles * ((p.N + C::kTileOut - 1) / C::kTileOut) * ((p.K + kKB - 1) / kKB);
   if (blocks < pairs) pairs = (int)blocks;
   cfg.gridDim = dim3((unsigned)(2 * pairs));
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, pair_kernel<kDown, kLow>, p, w0, w1, high, r16);
+  return cudaLaunchKernelEx(&cfg, pair_kernel<kDown, kLow, kWide>, p, w0, w1, high, r16);
 }
 
 template <bool kLow>
@@ -648,11 +663,18 @@ cudaError_t launch_ffn(const MoeFfnArgs& a, cudaStream_t s) {
   }
   const int part_n = kLow ? kMoeLowTile : moe_part_rows(a.rows);
   const Args gu{a.offsets, a.rows, a.E, a.h, a.d, a.act, static_cast<bf16*>(a.v), a.part, part_n, a.ctr, a.err};
-  cudaError_t e = launch_pair<false, kLow>(gu, tm_g, tm_u, tm_x, tm_x16, s);
+  cudaError_t e = launch_pair<false, kLow, false>(gu, tm_g, tm_u, tm_x, tm_x16, s);
   if (e != cudaSuccess) return e;
   const Args dn{a.offsets, a.rows, a.E,    a.d,    a.h, a.act, static_cast<bf16*>(a.ys), a.part,
                 part_n,    a.ctr + 2 * kMoeMaxPairs, a.err};
-  return launch_pair<true, kLow>(dn, tm_d, tm_d, tm_v, tm_v16, s);
+  if constexpr (!kLow) {
+    // Half as many tiles twice as wide, as long as they go round half the pairs when the rows spread
+    // over the experts.  8 experts, d 4096, h 14336: 256 rows 459 us (256 columns: 499), 8192 rows
+    // 2073 (2335); 16 wide tiles (8 experts of 128 rows, d 1024, h 1024) 41 us (37).
+    const int spread = a.E < a.rows ? a.E : a.rows, high = (a.rows + kMoeTileRows - 1) / kMoeTileRows;
+    if ((long long)(spread > high ? spread : high) * ((a.d + 511) / 512) * 4 >= sm_count()) return launch_pair<true, false, true>(dn, tm_d, tm_d, tm_v, tm_v16, s);
+  }
+  return launch_pair<true, kLow, false>(dn, tm_d, tm_d, tm_v, tm_v16, s);
 }
 
 }  // namespace

@@ -227,6 +227,17 @@ def test_ffn(d, h, counts, spare, act):
     check_ffn(make_experts(g, len(counts), d, h, act), rnd(g, sum(counts), d), counts, act, spare)
 
 
+# Tiles left over and cut along the contraction: into parts (few rows; many rows), as one run over the
+# pairs; whole rounds before them; wide down tiles with a ragged last block.
+@pytest.mark.parametrize("d,h,counts", [
+    (4096, 512, [40]), (4096, 512, [300, 40]), (1024, 4096, [5, 0, 9]), (4096, 2560, [2, 1, 30, 0, 8, 4]),
+    (2048, 4104, [33, 1]), (512, 2048, [600, 900, 10, 1300]), (1032, 264, [70, 3, 0, 300, 1, 8, 257, 31, 64, 5, 9, 2, 128, 40]),
+    (264, 520, [10 + 3 * i for i in range(45)]), (8200, 128, [90, 200, 33]), (64, 8200, [400])])
+def test_ffn_split_tiles(d, h, counts):
+    g = gen(d + h)
+    check_ffn(make_experts(g, len(counts), d, h), rnd(g, sum(counts), d), counts)
+
+
 def test_ffn_many_experts():
     g = gen(3)
     counts = [int(c) for c in torch.randint(0, 4, (512,), generator=torch.Generator().manual_seed(1))]
