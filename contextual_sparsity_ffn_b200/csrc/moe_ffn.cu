@@ -305,20 +305,20 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow, kWide>::kThreads, 1)
     tmem_alloc_pair(&s_tmem, C::kColumns);
     tmem_relinquish_pair();
   }
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync_all();  // both CTAs' barriers and TMEM are set up
-  tc_fence_after();
-  const uint32_t tmem = s_tmem;
   // The gate/up kernel lets the down kernel start only after its own wait, so what came before the
   // gate/up kernel is complete when the down kernel starts: the offsets (and the weights) may be read
   // before the down kernel's wait, v after it.
   if (!kDown) pdl_wait_prior();
   pdl_trigger();
   for (int e = threadIdx.x; e <= a.E; e += C::kThreads) s_plan.lo[e] = __ldcg(a.offsets + e);
+  tc_fence_before();
   __syncthreads();
+  cluster_arrive_all();
   if (warp == 0) make_plan<C::kTileRows>(a, &s_plan);
   __syncthreads();
+  cluster_wait_all();  // both CTAs' barriers and TMEM are set up
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
   const int n_tiles = s_plan.tp[a.E] * mb;
 
   if (warp == 0) {
@@ -526,18 +526,19 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow, kWide>::kThreads, 1)
 
       const int parts = w.parts();
       uint32_t* ctr = a.ctr + 2 * w.left_tile() + rank;
-      __threadfence();
+      // the barriers order the CTA's stores and loads around one thread's fences
       named_sync(2, kEpiWarps * kWarp);
       if (threadIdx.x == 2 * kWarp) {
+        __threadfence();
         s_last = atomicAdd(ctr, 1u) + 1u == (uint32_t)parts;
         if (s_last) *ctr = 0u;
+        __threadfence();
       }
       named_sync(2, kEpiWarps * kWarp);
       if (!s_last) {
         named_sync(2, kEpiWarps * kWarp);  // s_last is written again by the next part
         continue;
       }
-      __threadfence();
       for (int c = c0; c < c1; c += kChunk) {
         float g[kChunk], u[kChunk];
 #pragma unroll
