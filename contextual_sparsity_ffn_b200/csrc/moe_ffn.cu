@@ -42,8 +42,8 @@
 //
 // Warp roles: warp 0 issues the copies, warp 1 owns TMEM and (even CTA) issues the MMAs, the other
 // 8 run the epilogue: TMEM lane = output, column = row, two warps per lane quarter, each half of the
-// columns.  Neighbouring lanes exchange one value of each column pair so that a lane stores two
-// adjacent outputs (4 bytes).
+// columns.  While a tile with two accumulators is drained no MMA runs, so the epilogue keeps the next
+// columns' TMEM loads under way and stores 8 bytes a lane.
 //
 // Row bounds come from the device: `offsets` is clamped to 0 .. rows and to ascending order when it is
 // read, so no offsets can lead an access outside the buffers.  Every wait is bounded (one second)
@@ -259,10 +259,16 @@ struct Ring {
   }
 };
 
-// SiLU for a value that is rounded to bf16 next: the fast exponential and division (a few fp32
-// steps) are far below that rounding.
+// The activation of a value that goes on in bf16.  SiLU as z * 1 / (1 + 2^(-z log2 e)) on the
+// approximate exponential and reciprocal instructions: a few fp32 steps, far below the rounding, and
+// with 4 other operations per value the least the epilogue can do (it is bound by these two: 16
+// cycles per warp and value of the special-function units).
 __device__ __forceinline__ float act_fast(float z, int act) {
-  return act == CSFFN_ACT_SILU ? __fdividef(z, 1.0f + __expf(-z)) : fmaxf(z, 0.0f);
+  if (act != CSFFN_ACT_SILU) return fmaxf(z, 0.0f);
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.44269504f * z));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return z * r;
 }
 
 template <bool kDown, bool kLow, bool kWide>
@@ -444,6 +450,7 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow, kWide>::kThreads, 1)
     const int quarter = warp & 3, side = (warp - 2) >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
     const int out_lane = 32 * quarter + lane;
+    const bool odd = lane & 1, high = lane & 2;
     const size_t part_acc = (size_t)a.part_n / 4 * 128, part_place = C::kAccs * part_acc * 4;  // float4s, floats
     Buffers<kDown, kLow, kWide> buf;
     Items w(pair, pairs, n_kb, n_tiles, kLow);
@@ -456,26 +463,39 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow, kWide>::kThreads, 1)
       if (!named_all(1, kEpiWarps * kWarp, got)) break;
       tc_fence_after();
       const uint32_t acc = lane_base + buf.column();
-      const int o = t.m * C::kTileOut + (int)rank * 128 + out_lane;
+      const int o = t.m * C::kTileOut + (int)rank * 128 + (out_lane & ~3);  // N is a multiple of 8
       const int width = kLow ? C::kTileRows / C::kSides : t.n / C::kSides, c0 = side * width, c1 = c0 + width;
 
-      // a chunk of columns' results to memory: even lanes keep column k of their own and the next output, odd
-      // lanes column k + 1
-      auto put16 = [&](int c, const float (&g)[kChunk], int out) {
+      // A chunk of columns' results to memory.  `p`: column pairs of this lane's output.  Two exchanges
+      // turn 4 outputs x 4 columns of neighbouring lanes around, so that a lane stores 4 adjacent
+      // outputs (8 bytes) of column 4 j + lane % 4.
+      auto store = [&](int c, const uint32_t (&p)[kChunk / 2], int out, bf16* base) {
 #pragma unroll
-        for (int k = 0; k < kChunk; k += 2) {
-          const float give = (lane & 1) ? g[k] : g[k + 1];
-          const float take = __shfl_xor_sync(0xffffffffu, give, 1);
-          const float first = (lane & 1) ? take : g[k], second = (lane & 1) ? g[k + 1] : take;
-          const __nv_bfloat162 v = __floats2bfloat162_rn(first, second);
-          const int row = t.row0 + c + k + (lane & 1);
-          if (row < t.row1 && out < a.N) {
-            __nv_bfloat162* at = reinterpret_cast<__nv_bfloat162*>(a.out + (size_t)row * a.N + (out & ~1));
-            *at = v;
-            if constexpr (kLow && !kDown)
-              at[(size_t)a.rows * a.N / 2] =
-                  __floats2bfloat162_rn(first - __low2float(v), second - __high2float(v));
+        for (int j = 0; j < kChunk / 4; ++j) {
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, __byte_perm(p[2 * j], p[2 * j + 1], odd ? 0x5410 : 0x7632), 1);
+          const uint32_t a0 = __byte_perm(p[2 * j], got, odd ? 0x3254 : 0x5410);
+          const uint32_t a1 = __byte_perm(p[2 * j + 1], got, odd ? 0x3276 : 0x7610);
+          const uint32_t back = __shfl_xor_sync(0xffffffffu, high ? a0 : a1, 2);
+          const int row = t.row0 + c + 4 * j + (lane & 3);
+          if (row < t.row1 && out < a.N)
+            *reinterpret_cast<uint2*>(base + (size_t)row * a.N + out) = high ? make_uint2(back, a1) : make_uint2(a0, back);
+        }
+      };
+      auto put16 = [&](int c, const float (&g)[kChunk], int out) {
+        uint32_t p[kChunk / 2];
+#pragma unroll
+        for (int k = 0; k < kChunk / 2; ++k) {
+          const __nv_bfloat162 v = __floats2bfloat162_rn(g[2 * k], g[2 * k + 1]);
+          p[k] = reinterpret_cast<const uint32_t&>(v);
+        }
+        store(c, p, out, a.out);
+        if constexpr (kLow && !kDown) {  // what the rounding left
+#pragma unroll
+          for (int k = 0; k < kChunk / 2; ++k) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(g[2 * k] - bf16lo(p[k]), g[2 * k + 1] - bf16hi(p[k]));
+            p[k] = reinterpret_cast<const uint32_t&>(v);
           }
+          store(c, p, out, a.out + (size_t)a.rows * a.N);
         }
       };
       auto put = [&](int c, float (&g)[kChunk], const float (&u)[kChunk]) {
@@ -492,13 +512,13 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow, kWide>::kThreads, 1)
         return reinterpret_cast<float4*>(a.part + (size_t)(place * 2 + (int)rank) * part_place) + out_lane;
       };
       float4* mine = whole ? nullptr : part_at(w.my_place());
-      for (int c = c0; c < c1; c += kChunk) {
-        float g[kChunk], u[kChunk];
+      auto load = [&](int c, float (&g)[kChunk], float (&u)[kChunk]) {
         __syncwarp();
         tmem_ld16(acc + (uint32_t)c, g);
         if constexpr (C::kAccs == 2) tmem_ld16(acc + C::kUp + (uint32_t)c, u);
         if constexpr (C::kParts == 2) tmem_ld16(acc + 32u + (uint32_t)c, u);
-        tmem_ld_wait();
+      };
+      auto take = [&](int c, float (&g)[kChunk], float (&u)[kChunk]) {
         if constexpr (C::kParts == 2) {  // the low part of v's share
 #pragma unroll
           for (int k = 0; k < kChunk; ++k) g[k] += u[k];
@@ -514,6 +534,23 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow, kWide>::kThreads, 1)
                      make_float4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]));
           }
         }
+      };
+      auto ready = [&](float (&g)[kChunk], float (&u)[kChunk]) {
+        tmem_ld_wait(g);
+        if constexpr (C::kAccs + C::kParts > 2) tmem_ld_wait(u);
+      };
+      // the next chunk's loads are under way while one is worked on
+      float g0[kChunk], u0[kChunk], g1[kChunk], u1[kChunk];
+      load(c0, g0, u0);
+      for (int c = c0; c < c1; c += 2 * kChunk) {
+        ready(g0, u0);
+        const bool more = c + kChunk < c1;
+        if (more) load(c + kChunk, g1, u1);
+        take(c, g0, u0);
+        if (!more) break;
+        ready(g1, u1);
+        if (c + 2 * kChunk < c1) load(c + 2 * kChunk, g0, u0);
+        take(c + kChunk, g1, u1);
       }
       tc_fence_before();
       __syncwarp();
