@@ -539,25 +539,35 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow, kWide>::kThreads, 1)
         tmem_ld_wait(g);
         if constexpr (C::kAccs + C::kParts > 2) tmem_ld_wait(u);
       };
+      // A tile that holds both buffers gives them up as soon as its last columns are in registers: the
+      // next tile's MMAs wait for that.
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_cluster(map_to_rank(&acce[buf.b], 0));
+          if (buf.both) mbar_arrive_cluster(map_to_rank(&acce[1], 0));
+        }
+      };
       // the next chunk's loads are under way while one is worked on
       float g0[kChunk], u0[kChunk], g1[kChunk], u1[kChunk];
       load(c0, g0, u0);
       for (int c = c0; c < c1; c += 2 * kChunk) {
+        const bool two = c + kChunk < c1, more = c + 2 * kChunk < c1;
         ready(g0, u0);
-        const bool more = c + kChunk < c1;
-        if (more) load(c + kChunk, g1, u1);
+        if (two) load(c + kChunk, g1, u1);
+        if (!more && buf.both) {
+          if (two) ready(g1, u1);
+          release();
+        }
         take(c, g0, u0);
-        if (!more) break;
-        ready(g1, u1);
-        if (c + 2 * kChunk < c1) load(c + 2 * kChunk, g0, u0);
-        take(c + kChunk, g1, u1);
+        if (two) {
+          if (more || !buf.both) ready(g1, u1);
+          if (more) load(c + 2 * kChunk, g0, u0);
+          take(c + kChunk, g1, u1);
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive_cluster(map_to_rank(&acce[buf.b], 0));
-        if (buf.both) mbar_arrive_cluster(map_to_rank(&acce[1], 0));
-      }
+      if (!buf.both) release();
       buf.done();
       if (whole) continue;
 
