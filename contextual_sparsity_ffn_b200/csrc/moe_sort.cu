@@ -9,10 +9,13 @@
 // chunk for itself in shared memory and gathers its own tokens' rows.
 //
 // Gather: one pass over the tokens: a token's row is read once and written to the positions of its
-// slots (d bytes read + k d written, against k d + k d for a gather by position).
+// slots (d bytes read + k d written, against k d + k d for a gather by position).  8192 tokens x 8 of
+// 64 experts, d 2048 bf16: the three kernels 53 us, of which the gather is 43 (41 at the copy rate);
+// 13 tokens in the one kernel: 4.5 us, the latency of its chain of loads, counts and stores.
 //
 // Combine: one pass over the tokens: each thread owns 8 columns and adds the token's k rows in slot
-// order in fp32, so the sum does not depend on timing (no atomics).
+// order in fp32, so the sum does not depend on timing (no atomics).  Bound by memory: the same
+// tokens 46 us (41 at the copy rate).
 #include "common.cuh"
 #include "kernels.h"
 #include "tcgen05.cuh"

@@ -341,7 +341,8 @@ typedef struct {
 typedef enum { CSFFN_ROUTE_SOFTMAX = 0, CSFFN_ROUTE_SIGMOID = 1 } csffn_route_score;
 
 /* Router projection: logits[t, e] = sum_c x[t, c] * w_router[e, c], fp32 sums.
- *   x: bf16 [T, d]; w_router: bf16 [E, d]; logits: fp32 [T, E].  d % 8 == 0, both 16-byte aligned. */
+ *   x: bf16 [T, d]; w_router: bf16 [E, d]; logits: fp32 [T, E].  d % 8 == 0, both 16-byte aligned.
+ *   There is no workspace: if a bounded wait ran out, the tile's logits are NaN. */
 csffn_status csffn_moe_logits(const void* x, const void* w_router, int T, int E, int d, float* logits,
                               void* stream);
 
@@ -370,7 +371,8 @@ size_t csffn_moe_dispatch_workspace_size(int max_rows, int n_experts);
  *   order[p] = slot at sorted position p (int32 [T * k]); pos[s] = sorted position of slot s, or -1
  *   (int32 [T, k]); xs[p, :] = x[order[p] / k, :] ([T * k, d] in xdtype).
  *   Entries of order and rows of xs at and behind offsets[E] are left as they were.
- *   x: [T, d] in xdtype (csffn_dtype).  1 <= k <= CSFFN_MAX_TOPK, 1 <= E <= CSFFN_MAX_EXPERTS.
+ *   x: [T, d] in xdtype (csffn_dtype), which must not overlap xs.
+ *   1 <= k <= CSFFN_MAX_TOPK, 1 <= E <= CSFFN_MAX_EXPERTS.
  *   T == 0: writes offsets = 0. */
 csffn_status csffn_moe_dispatch(const void* x, int xdtype, const int32_t* ids, int T, int k, int E, int d,
                                 int32_t* offsets, int32_t* order, int32_t* pos, void* xs, void* ws,
@@ -393,7 +395,7 @@ csffn_status csffn_moe_ffn_forward(const csffn_moe_layer* layer, const void* xs,
 /* Expert outputs back in token order: out[t, :] = sum_j weights[t, j] * ys[pos[t, j], :] in fp32,
  * written (or accumulated) by out_mode; entries with pos outside [0, rows) are skipped, whatever
  * their weight.  ys: bf16 [rows, d]; pos: int32 [T, k]; weights: fp32 [T, k], or NULL for weights
- * of 1; out: [T, d] in the dtype of out_mode. */
+ * of 1; out: [T, d] in the dtype of out_mode, not overlapping ys. */
 csffn_status csffn_moe_combine(const void* ys, const int32_t* pos, const float* weights, int T, int k, int rows, int d,
                                void* out, int out_mode, void* stream);
 
