@@ -206,7 +206,7 @@ cudaError_t launch_timeout_selftest(uint64_t* flag, uint32_t* err, int spin_limi
 struct MoeWs {          // workspace of csffn_moe_dispatch and csffn_moe_ffn_forward
   size_t err;           // uint32 error word, where WsLayout has it (csffn_check_status)
   size_t hist;          // dispatch: int32 [chunks][E] expert counts per chunk of slots
-  size_t ctr;           // ffn: uint32 [2 kernels][kMoeMaxPairs][2] split tiles' counters, zero between calls
+  size_t ctr;           // ffn: uint32 [2 kernels][2 * kMoeMaxPairs] split tiles' counters, zero between calls
   size_t v;             // ffn: bf16 [moe_v_rows(rows, E)][h]
   size_t part;          // ffn: fp32 split tiles' parts, moe_part_floats(rows)
   size_t total;
@@ -223,12 +223,9 @@ inline size_t moe_v_rows(int rows, int E) {
   return (size_t)(rows > low ? rows : low);
 }
 inline int moe_part_rows(int rows) { return rows >= kMoeTileRows ? kMoeTileRows : (rows + 31) / 32 * 32; }
-// Split tiles' parts, [places][2 CTAs][2 accumulators][rows of a tile][128]: a place per pair, or two
-// with few rows per tile.
-inline size_t moe_part_floats(int rows) {
-  const int tall = kMoeMaxPairs * moe_part_rows(rows), low = 2 * kMoeMaxPairs * kMoeLowTile;
-  return (size_t)(tall > low ? tall : low) * 2 * 2 * 128;
-}
+// Split tiles' parts: [pairs][2 CTAs][2 accumulators][rows of a tile][128]; with few rows two places per
+// CTA, [2 CTAs of a pair][2 places][32 rows][128].
+inline size_t moe_part_floats(int rows) { return (size_t)kMoeMaxPairs * 2 * 2 * moe_part_rows(rows) * 128; }
 constexpr int kMoeChunk = 1024;     // least slots per counting chunk
 constexpr int kMoeMaxChunks = 256;  // most chunks: each placing CTA adds up all chunks' counts
 inline int moe_chunk_slots(int rows) {
@@ -287,6 +284,7 @@ struct MoeFfnArgs {
   uint32_t* err;
 };
 cudaError_t launch_moe_ffn(const MoeFfnArgs& a, cudaStream_t s);
+cudaError_t launch_moe_ffn_low(const MoeFfnArgs& a, cudaStream_t s);  // few rows per expert
 
 struct BlockNormArgs {
   const float* h;

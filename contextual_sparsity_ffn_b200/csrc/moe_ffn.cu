@@ -3,6 +3,8 @@
 //   gate/up: v[p, i] = act(xs_p . W_gate[e, i]) * (xs_p . W_up[e, i])      (bf16 into the workspace)
 //   down:    ys[p, c] = sum_i v[p, i] W_down^T[e, i, c]
 //
+// For experts with many rows each; moe_ffn_low.cu is for few.  v is rounded once to bf16.
+//
 // Both kernels compute D[output, row] with the weights as the M side: a tile is 256 outputs
 // (neurons, or columns of ys) x up to 256 rows of one expert, and a pair of CTAs works on it
 // (cta_group::2, M = 256: 128 outputs each).  The rows are the N side because an expert's row count
@@ -14,19 +16,12 @@
 // way from L2 to the SMs: 64 bytes a cycle and SM for 256 x 256 at the tensor cores' full rate, 48 for
 // 512 x 256.
 //
-// Few rows per expert (kLow) is the weights' stream and little else: tiles of 32 rows, so that a stage
-// is nearly all weights.  v is kept as a bf16 high part and a bf16 low part there (v - high), the two
-// halves of the down product's N side: about 16 bits of v reach the product at no cost in time.  With
-// many rows, where the products are the time, v is rounded once to bf16.
-//
 // Work split: whole tiles go round the pairs as long as there is one for every pair.  The R tiles
 // left over (all of them in a decode step) would leave pairs idle, so they are cut along the
-// contraction where that pays.  Up to half as many tiles as pairs: each into S = pairs / R parts (at
-// most kMaxParts), one part per pair.  More, with few rows: the tiles' k-blocks, in order, form one
-// run that is divided evenly among the pairs (a pair holds parts of at most two tiles).  A pair with a
-// part stores its fp32 accumulators in the workspace and counts up the tile's counter; the last one adds
-// the parts in their order (the same bits whoever is last), writes the tile and clears the counter.
-// No pair waits for another.
+// contraction where that pays: up to half as many tiles as pairs, each into S = pairs / R parts (at
+// most kMaxPartsTall), one part per pair.  A pair with a part stores its fp32 accumulators in the
+// workspace and counts up the tile's counter; the last one adds the parts in their order (the same
+// bits whoever is last), writes the tile and clears the counter.  No pair waits for another.
 //
 // Row split: an expert with n rows takes ceil(n / 256) tiles of equal height (rounded up to 32).
 // Tiles are numbered expert by expert, output block by output block, row tiles innermost, so the
@@ -48,188 +43,36 @@
 // Row bounds come from the device: `offsets` is clamped to 0 .. rows and to ascending order when it is
 // read, so no offsets can lead an access outside the buffers.  Every wait is bounded (one second)
 // and records the timeout.
-#include "common.cuh"
-#include "fused_end.cuh"
-#include "kernels.h"
-#include "tcgen05.cuh"
+#include "moe_ffn.cuh"
 
 namespace csffn {
 namespace {
 
-constexpr int kKB = 64;                            // contraction elements per stage
-constexpr uint32_t kRowBytes = kKB * 2;            // one row of a stage's tile
-constexpr uint32_t kWBox = 128 * kRowBytes;        // one CTA's 128 outputs x 64: 16 KB
-constexpr int kMaxParts = 8, kMaxPartsTall = 4;    // parts of a tile
-constexpr int kMinSaved = 16, kMinSavedTall = 24;  // k-blocks
+using namespace moe;
 
-template <bool kDown, bool kLow, bool kWide>
+constexpr uint32_t kWBox = 128 * kRowBytes;  // one CTA's 128 outputs x 64: 16 KB
+
+template <bool kDown, bool kWide>
 struct Cfg {
   static constexpr int kTileOut = kWide ? 512 : 256;                   // outputs per tile
-  static constexpr int kTileRows = kLow ? kMoeLowTile : kMoeTileRows;  // most rows per tile
-  static constexpr int kParts = kDown && kLow ? 2 : 1;                 // high and low part of v
   static constexpr int kAccs = kDown && !kWide ? 1 : 2;                // gate and up, or two blocks of 256 columns
   static constexpr int kEpiWarps = 8;
   static constexpr int kSides = kEpiWarps / 4;         // shares of a tile's columns
   static constexpr int kThreads = (2 + kEpiWarps) * kWarp;
   static constexpr uint32_t kW = kAccs * kWBox;
-  static constexpr uint32_t kStage = kW + (uint32_t)(kParts * kTileRows / 2) * kRowBytes;
-  static constexpr int kStages = kLow ? (kDown ? 10 : 6) : (kAccs == 1 ? 6 : 4);
+  static constexpr uint32_t kStage = kW + (uint32_t)(kMoeTileRows / 2) * kRowBytes;
+  static constexpr int kStages = kAccs == 1 ? 6 : 4;
   static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
   // Accumulator columns: two buffers; the second accumulator is kUp columns behind the first.  With two
   // accumulators a tile of more than 128 rows takes both buffers.
-  static constexpr uint32_t kBuffer = kLow ? 32u * kParts : kAccs == 1 ? 256u : 128u;
+  static constexpr uint32_t kBuffer = kAccs == 1 ? 256u : 128u;
   static constexpr uint32_t kUp = 2 * kBuffer;
-  static constexpr uint32_t kColumns = kLow ? 128 : 512;
-};
-
-struct Args {
-  const int32_t* offsets;
-  int rows, E, N, K, act;  // N outputs per expert, K contraction
-  bf16* out;               // [rows, N]; gate/up with few rows: [2][rows, N], high and low parts
-  float* part;             // [places][2 CTAs][accumulators][part_n / 4][128][4] split tiles' parts
-  int part_n;              // most rows of a tile of this call
-  uint32_t* ctr;           // [pairs][2]: parts done of the split tiles
-  uint32_t* err;
-};
-
-// Every expert's rows and tiles, worked out once per CTA: lo[e] .. lo[e + 1] are expert e's rows,
-// tp[e] the row tiles of the experts before it.
-struct Plan {
-  int lo[CSFFN_MAX_EXPERTS + 1];
-  int tp[CSFFN_MAX_EXPERTS + 1];
-};
-
-// By one warp, from the raw offsets in p->lo: each lane takes a few consecutive entries.
-template <int kTileRows>
-__device__ void make_plan(const Args& a, Plan* p) {
-  const int lane = threadIdx.x & 31, per = (a.E + kWarp) / kWarp;  // E + 1 entries
-  const int e0 = min(lane * per, a.E + 1), e1 = min(e0 + per, a.E + 1);
-  int top = 0;  // the largest offset up to here: ascending order
-  for (int e = e0; e < e1; ++e) {
-    top = max(top, min(p->lo[e], a.rows));
-    p->lo[e] = top;
-  }
-#pragma unroll
-  for (int o = 1; o < kWarp; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, top, o);
-    if (lane >= o) top = max(top, u);
-  }
-  int before = __shfl_up_sync(0xffffffffu, top, 1);  // of the entries of lower lanes
-  if (lane == 0) before = 0;
-  // entry e closes expert e - 1
-  int tiles = 0, prev = before;
-  for (int e = e0; e < e1; ++e) {
-    const int v = max(p->lo[e], before);
-    p->lo[e] = v;
-    if (e > 0) tiles += (v - prev + kTileRows - 1) / kTileRows;
-    p->tp[e] = tiles;
-    prev = v;
-  }
-  int sum = tiles;
-#pragma unroll
-  for (int o = 1; o < kWarp; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, sum, o);
-    if (lane >= o) sum += u;
-  }
-  for (int e = e0; e < e1; ++e) p->tp[e] += sum - tiles;
-}
-
-struct Tile {
-  int e, m;        // expert, output block
-  int row0, row1;  // rows
-  int n;           // N of its MMAs: the rows rounded up to 32
-  bool once;       // the expert's weights are read by this row tile alone
-};
-
-__device__ __forceinline__ Tile find_tile(const Plan& p, int E, int mb, int i) {
-  const int q = i / mb;
-  int a = 0, b = E;  // tp[a] <= q < tp[b]
-  while (b - a > 1) {
-    const int c = (a + b) >> 1;
-    if (p.tp[c] <= q)
-      a = c;
-    else
-      b = c;
-  }
-  const int nt = p.tp[a + 1] - p.tp[a], r = i - p.tp[a] * mb;
-  const int cnt = p.lo[a + 1] - p.lo[a];
-  const int height = ((cnt + nt - 1) / nt + 31) / 32 * 32;
-  Tile t;
-  t.e = a;
-  t.m = r / nt;
-  t.row0 = p.lo[a] + (r % nt) * height;
-  t.row1 = min(t.row0 + height, p.lo[a + 1]);
-  t.n = (t.row1 - t.row0 + 31) / 32 * 32;
-  t.once = nt == 1;
-  return t;
-}
-
-// The work of one pair in order: (tile, k-blocks [kb0, kb1)).
-struct Items {
-  int pair, pairs, n_kb, n_whole, left;  // tiles [0, n_whole) go round whole, `left` after them
-  int split;                             // parts of a left-over tile, or 0: one run for all of them
-  int next;                              // next whole tile
-  int it, it1;                           // this pair's k-blocks of the run
-  int tile, kb0, kb1;                    // the current item
-  __device__ Items(int pair_, int pairs_, int n_kb_, int n_tiles, bool low)
-      : pair(pair_), pairs(pairs_), n_kb(n_kb_) {
-    n_whole = n_tiles / pairs * pairs;
-    left = n_tiles - n_whole;
-    // A part costs its accumulators' way through L2 and about 4 us at the end, as much as 16 k-blocks
-    // of a low tile or 20 of a tall one: cut only where that many k-blocks less are to be done.
-    split = left ? min(min(pairs / left, low ? kMaxParts : kMaxPartsTall), n_kb) : 1;
-    if (n_kb - n_kb / split < (low ? kMinSaved : kMinSavedTall)) split = 1;
-    if (low && left && pairs / left == 1 && n_kb - (int)((long long)n_kb * left / pairs) >= kMinSaved) split = 0;
-    next = pair;
-    it = split == 0 ? run_start(pair) : 0;
-    it1 = split == 0 ? run_start(pair + 1) : 0;
-  }
-  // the run: left * n_kb k-blocks, more than half as many tiles as pairs, so no pair's share is empty
-  __device__ int run_start(int q) const { return (int)((long long)q * left * n_kb / pairs); }
-  __device__ int run_owner(int j) const { return (int)(((long long)(j + 1) * pairs - 1) / (left * n_kb)); }
-  __device__ bool advance() {
-    kb0 = 0;
-    kb1 = n_kb;
-    tile = next;
-    if (next < n_whole) {
-      next += pairs;
-      return true;
-    }
-    if (split == 0) {
-      if (it >= it1) return false;
-      tile = n_whole + it / n_kb;
-      kb0 = it % n_kb;
-      kb1 = min(n_kb, kb0 + (it1 - it));
-      it += kb1 - kb0;
-      return true;
-    }
-    const int q = next - n_whole;  // this pair's number, until its last item is out
-    if (q >= left * split) return false;
-    next = 0x7fffffff;
-    tile = n_whole + q % left;
-    kb0 = (q / left) * n_kb / split;
-    kb1 = (q / left + 1) * n_kb / split;
-    return true;
-  }
-  __device__ bool whole() const { return kb1 - kb0 == n_kb; }
-  __device__ int left_tile() const { return tile - n_whole; }
-  // the parts of the current tile, and where part r is kept (at most 2 * pairs places)
-  __device__ int first_pair() const { return run_owner(left_tile() * n_kb); }
-  __device__ int parts() const { return split ? split : run_owner(left_tile() * n_kb + n_kb - 1) - first_pair() + 1; }
-  __device__ int place(int r) const {
-    if (split) return left_tile() * split + r;
-    const int q = first_pair() + r;
-    return 2 * q + (run_start(q) >= left_tile() * n_kb ? 0 : 1);
-  }
-  __device__ int my_place() const {
-    if (split) return left_tile() * split + pair / left;
-    return 2 * pair + (run_start(pair) >= left_tile() * n_kb ? 0 : 1);
-  }
+  static constexpr uint32_t kColumns = 512;
 };
 
 // Which accumulator buffers an item takes, and how often each was taken before: every role counts the
 // same items, so they agree on the barriers' phases.
-template <bool kDown, bool kLow, bool kWide>
+template <bool kDown, bool kWide>
 struct Buffers {
   int turn = 0;
   uint32_t used0 = 0, used1 = 0;
@@ -237,7 +80,7 @@ struct Buffers {
   bool both;  // it takes both
   __device__ uint32_t used() const { return b ? used1 : used0; }
   __device__ void take(int n) {
-    both = Cfg<kDown, kLow, kWide>::kAccs == 2 && !kLow && n > 128;
+    both = Cfg<kDown, kWide>::kAccs == 2 && n > 128;
     b = both ? 0 : turn;
     if (!both) turn ^= 1;
   }
@@ -245,37 +88,14 @@ struct Buffers {
     if (b == 0) ++used0;
     if (b == 1 || both) ++used1;
   }
-  __device__ uint32_t column() const { return Cfg<kDown, kLow, kWide>::kBuffer * b; }
+  __device__ uint32_t column() const { return Cfg<kDown, kWide>::kBuffer * b; }
 };
 
-struct Ring {
-  int slot = 0;
-  uint32_t round = 0;
-  __device__ void next(int n) {
-    if (++slot == n) {
-      slot = 0;
-      ++round;
-    }
-  }
-};
-
-// The activation of a value that goes on in bf16.  SiLU as z * 1 / (1 + 2^(-z log2 e)) on the
-// approximate exponential and reciprocal instructions: a few fp32 steps, far below the rounding, and
-// with 4 other operations per value the least the epilogue can do (it is bound by these two: 16
-// cycles per warp and value of the special-function units).
-__device__ __forceinline__ float act_fast(float z, int act) {
-  if (act != CSFFN_ACT_SILU) return fmaxf(z, 0.0f);
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.44269504f * z));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-  return z * r;
-}
-
-template <bool kDown, bool kLow, bool kWide>
-__global__ void __launch_bounds__(Cfg<kDown, kLow, kWide>::kThreads, 1)
+template <bool kDown, bool kWide>
+__global__ void __launch_bounds__(Cfg<kDown, kWide>::kThreads, 1)
     pair_kernel(const Args a, const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ CUtensorMap tm_w1,
-                const __grid_constant__ CUtensorMap tm_high, const __grid_constant__ CUtensorMap tm_r16) {
-  using C = Cfg<kDown, kLow, kWide>;
+                const __grid_constant__ CUtensorMap tm_r64, const __grid_constant__ CUtensorMap tm_r16) {
+  using C = Cfg<kDown, kWide>;
   constexpr int kStages = C::kStages, kEpiWarps = C::kEpiWarps, kChunk = 16;
   extern __shared__ __align__(1024) unsigned char moe_raw[];
   __shared__ __align__(8) uint64_t full[kStages], empty[kStages], accf[2], acce[2], drain;
@@ -293,8 +113,8 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow, kWide>::kThreads, 1)
   if (threadIdx.x == 0) {
     tma_prefetch_map(&tm_w0);
     if (!kDown) tma_prefetch_map(&tm_w1);
-    tma_prefetch_map(&tm_high);
-    if (!kLow) tma_prefetch_map(&tm_r16);
+    tma_prefetch_map(&tm_r64);
+    tma_prefetch_map(&tm_r16);
     s_abort = 0;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
@@ -320,7 +140,7 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow, kWide>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   cluster_arrive_all();
-  if (warp == 0) make_plan<C::kTileRows>(a, &s_plan);
+  if (warp == 0) make_plan<kMoeTileRows>(a, &s_plan);
   __syncthreads();
   cluster_wait_all();  // both CTAs' barriers and TMEM are set up
   tc_fence_after();
@@ -346,23 +166,16 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow, kWide>::kThreads, 1)
           tma_load_3d_pair(st + kWBox, &tm_w1, kb * kKB, out0, t.e, bar);
         }
       };
-      // bytes of a tile's rows in one CTA: half of them, or all rows of one part of v
-      auto row_bytes = [&](const Tile& t) { return (uint32_t)(kLow ? C::kParts * C::kTileRows / 2 : t.n / 2) * kRowBytes; };
       auto rows = [&](const Tile& t, int kb, unsigned char* st, uint32_t bar) {
-        if constexpr (kLow) {
-          const int row = kDown ? t.row0 + (int)rank * a.rows : t.row0 + (int)rank * (C::kTileRows / 2);
-          tma_load_2d_pair(st + C::kW, &tm_high, kb * kKB, row, bar);
-        } else {
-          const int half = t.n / 2, row0 = t.row0 + (int)rank * half;
-          int n = 0;
-          for (; n + 64 <= half; n += 64) tma_load_2d_pair(st + C::kW + n * kRowBytes, &tm_high, kb * kKB, row0 + n, bar);
-          for (; n < half; n += 16) tma_load_2d_pair(st + C::kW + n * kRowBytes, &tm_r16, kb * kKB, row0 + n, bar);
-        }
+        const int half = t.n / 2, row0 = t.row0 + (int)rank * half;
+        int n = 0;
+        for (; n + 64 <= half; n += 64) tma_load_2d_pair(st + C::kW + n * kRowBytes, &tm_r64, kb * kKB, row0 + n, bar);
+        for (; n < half; n += 16) tma_load_2d_pair(st + C::kW + n * kRowBytes, &tm_r16, kb * kKB, row0 + n, bar);
       };
       auto expect = [&](const Tile& t, int slot) {
-        if (rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * (C::kW + row_bytes(t)));
+        if (rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * (C::kW + (uint32_t)(t.n / 2) * kRowBytes));
       };
-      Items w(pair, pairs, n_kb, n_tiles, kLow);
+      Items w(pair, pairs, n_kb, n_tiles, false);
       bool more = w.advance();
       int first = 0;  // stages of the first item whose weights went out before the wait
       if (kDown && more) {
@@ -402,11 +215,11 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow, kWide>::kThreads, 1)
       // ---- MMA issuer
       Ring r;
       bool ok = true;
-      Buffers<kDown, kLow, kWide> buf;
-      Items w(pair, pairs, n_kb, n_tiles, kLow);
+      Buffers<kDown, kWide> buf;
+      Items w(pair, pairs, n_kb, n_tiles, false);
       while (ok && w.advance()) {
         const int n = find_tile(s_plan, a.E, mb, w.tile).n;
-        const uint32_t idesc = umma_idesc_bf16(256, kLow ? C::kParts * C::kTileRows : n, kDown);
+        const uint32_t idesc = umma_idesc_bf16(256, n, kDown);
         buf.take(n);
         if (buf.used() && !mbar_wait(&acce[buf.b], (buf.used() - 1) & 1, a.err, &s_abort)) break;
         if (buf.both && buf.used1 && !mbar_wait(&acce[1], (buf.used1 - 1) & 1, a.err, &s_abort)) break;
@@ -452,8 +265,8 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow, kWide>::kThreads, 1)
     const int out_lane = 32 * quarter + lane;
     const bool odd = lane & 1, high = lane & 2;
     const size_t part_acc = (size_t)a.part_n / 4 * 128, part_place = C::kAccs * part_acc * 4;  // float4s, floats
-    Buffers<kDown, kLow, kWide> buf;
-    Items w(pair, pairs, n_kb, n_tiles, kLow);
+    Buffers<kDown, kWide> buf;
+    Items w(pair, pairs, n_kb, n_tiles, false);
     while (w.advance()) {
       const Tile t = find_tile(s_plan, a.E, mb, w.tile);
       buf.take(t.n);
@@ -464,7 +277,7 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow, kWide>::kThreads, 1)
       tc_fence_after();
       const uint32_t acc = lane_base + buf.column();
       const int o = t.m * C::kTileOut + (int)rank * 128 + (out_lane & ~3);  // N is a multiple of 8
-      const int width = kLow ? C::kTileRows / C::kSides : t.n / C::kSides, c0 = side * width, c1 = c0 + width;
+      const int c0 = side * (t.n / C::kSides), c1 = c0 + t.n / C::kSides;
 
       // A chunk of columns' results to memory.  `p`: column pairs of this lane's output.  Two exchanges
       // turn 4 outputs x 4 columns of neighbouring lanes around, so that a lane stores 4 adjacent
@@ -489,14 +302,6 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow, kWide>::kThreads, 1)
           p[k] = reinterpret_cast<const uint32_t&>(v);
         }
         store(c, p, out, a.out);
-        if constexpr (kLow && !kDown) {  // what the rounding left
-#pragma unroll
-          for (int k = 0; k < kChunk / 2; ++k) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(g[2 * k] - bf16lo(p[k]), g[2 * k + 1] - bf16hi(p[k]));
-            p[k] = reinterpret_cast<const uint32_t&>(v);
-          }
-          store(c, p, out, a.out + (size_t)a.rows * a.N);
-        }
       };
       auto put = [&](int c, float (&g)[kChunk], const float (&u)[kChunk]) {
         if constexpr (!kDown) {
@@ -516,13 +321,8 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow, kWide>::kThreads, 1)
         __syncwarp();
         tmem_ld16(acc + (uint32_t)c, g);
         if constexpr (C::kAccs == 2) tmem_ld16(acc + C::kUp + (uint32_t)c, u);
-        if constexpr (C::kParts == 2) tmem_ld16(acc + 32u + (uint32_t)c, u);
       };
       auto take = [&](int c, float (&g)[kChunk], float (&u)[kChunk]) {
-        if constexpr (C::kParts == 2) {  // the low part of v's share
-#pragma unroll
-          for (int k = 0; k < kChunk; ++k) g[k] += u[k];
-        }
         if (whole) {
           put(c, g, u);
         } else {
@@ -537,7 +337,7 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow, kWide>::kThreads, 1)
       };
       auto ready = [&](float (&g)[kChunk], float (&u)[kChunk]) {
         tmem_ld_wait(g);
-        if constexpr (C::kAccs + C::kParts > 2) tmem_ld_wait(u);
+        if constexpr (C::kAccs == 2) tmem_ld_wait(u);
       };
       // A tile that holds both buffers gives them up as soon as its last columns are in registers: the
       // next tile's MMAs wait for that.
@@ -617,34 +417,9 @@ __global__ void __launch_bounds__(Cfg<kDown, kLow, kWide>::kThreads, 1)
   }
 }
 
-bool encode(CUtensorMap* tm, const void* base, int rank, const cuuint64_t* dim, const cuuint64_t* stride,
-            const cuuint32_t* box) {
-  TensorMapEncodeFn fn = tensor_map_encoder();
-  const cuuint32_t ones[3] = {1, 1, 1};
-  return fn && fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dim, stride, box, ones,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Weights [E, h, d], boxes of 64 x `high`.
-bool encode_weights(CUtensorMap* tm, const void* base, const MoeFfnArgs& a, cuuint32_t high) {
-  const cuuint64_t dim[3] = {(cuuint64_t)a.d, (cuuint64_t)a.h, (cuuint64_t)a.E};
-  const cuuint64_t stride[2] = {(cuuint64_t)a.d * 2, (cuuint64_t)a.h * a.d * 2};
-  const cuuint32_t box[3] = {64, high, 1};
-  return encode(tm, base, 3, dim, stride, box);
-}
-
-// Rows [rows, width], boxes of 64 x `high`.
-bool encode_rows(CUtensorMap* tm, const void* base, int rows, int width, cuuint32_t high) {
-  const cuuint64_t dim[2] = {(cuuint64_t)width, (cuuint64_t)rows};
-  const cuuint64_t stride[1] = {(cuuint64_t)width * 2};
-  const cuuint32_t box[2] = {64, high};
-  return encode(tm, base, 2, dim, stride, box);
-}
-
 // Pairs of CTAs to launch: as many as fit on the device at once (a static split over more would
 // wait for the first ones to finish), looked up once per device and kernel.
-template <bool kDown, bool kLow, bool kWide>
+template <bool kDown, bool kWide>
 cudaError_t resident_pairs(const cudaLaunchConfig_t& cfg, int* out) {
   static int cached[64] = {0};
   int dev = 0;
@@ -652,7 +427,7 @@ cudaError_t resident_pairs(const cudaLaunchConfig_t& cfg, int* out) {
   if (e != cudaSuccess) return e;
   int n = dev >= 0 && dev < 64 ? cached[dev] : 0;
   if (n == 0) {
-    e = cudaOccupancyMaxActiveClusters(&n, pair_kernel<kDown, kLow, kWide>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, pair_kernel<kDown, kWide>, &cfg);
     if (e != cudaSuccess) return e;
     if (n > kMoeMaxPairs) n = kMoeMaxPairs;
     if (n < 1) return cudaErrorInvalidConfiguration;
@@ -662,11 +437,11 @@ cudaError_t resident_pairs(const cudaLaunchConfig_t& cfg, int* out) {
   return cudaSuccess;
 }
 
-template <bool kDown, bool kLow, bool kWide>
-cudaError_t launch_pair(const Args& p, const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& high,
+template <bool kDown, bool kWide>
+cudaError_t launch_pair(const Args& p, const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& r64,
                         const CUtensorMap& r16, cudaStream_t s) {
-  using C = Cfg<kDown, kLow, kWide>;
-  cudaError_t e = cudaFuncSetAttribute(pair_kernel<kDown, kLow, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  using C = Cfg<kDown, kWide>;
+  cudaError_t e = cudaFuncSetAttribute(pair_kernel<kDown, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)C::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
@@ -684,51 +459,39 @@ cudaError_t launch_pair(const Args& p, const CUtensorMap& w0, const CUtensorMap&
   cfg.attrs = attr;
   cfg.numAttrs = 1;  // the cluster; the dependent launch is no part of the query
   int pairs = 0;
-  if ((e = resident_pairs<kDown, kLow, kWide>(cfg, &pairs)) != cudaSuccess) return e;
+  if ((e = resident_pairs<kDown, kWide>(cfg, &pairs)) != cudaSuccess) return e;
   // no more pairs than k-blocks there can be: every tile has a row, an expert at most one ragged tile
-  const long long row_tiles = (long long)(p.rows + C::kTileRows - 1) / C::kTileRows + (p.E < p.rows ? p.E : p.rows);
+  const long long row_tiles = (long long)(p.rows + kMoeTileRows - 1) / kMoeTileRows + (p.E < p.rows ? p.E : p.rows);
   const long long blocks = row_tiles * ((p.N + C::kTileOut - 1) / C::kTileOut) * ((p.K + kKB - 1) / kKB);
   if (blocks < pairs) pairs = (int)blocks;
   cfg.gridDim = dim3((unsigned)(2 * pairs));
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, pair_kernel<kDown, kLow, kWide>, p, w0, w1, high, r16);
-}
-
-template <bool kLow>
-cudaError_t launch_ffn(const MoeFfnArgs& a, cudaStream_t s) {
-  // boxes of the rows: all that a CTA takes of a tile (few rows), or 64 and 16 at a time
-  const cuuint32_t high_x = kLow ? kMoeLowTile / 2 : 64, high_v = kLow ? kMoeLowTile : 64;
-  CUtensorMap tm_g, tm_u, tm_x, tm_x16, tm_d, tm_v, tm_v16;
-  if (!encode_weights(&tm_g, a.W_gate, a, 128) || !encode_weights(&tm_u, a.W_up, a, 128) ||
-      !encode_weights(&tm_d, a.W_down_t, a, 64) || !encode_rows(&tm_x, a.xs, a.rows, a.d, high_x) ||
-      !encode_rows(&tm_v, a.v, kLow ? 2 * a.rows : a.rows, a.h, high_v))
-    return cudaErrorInvalidValue;
-  if (kLow) {
-    tm_x16 = tm_x;
-    tm_v16 = tm_v;
-  } else if (!encode_rows(&tm_x16, a.xs, a.rows, a.d, 16) || !encode_rows(&tm_v16, a.v, a.rows, a.h, 16)) {
-    return cudaErrorInvalidValue;
-  }
-  const int part_n = kLow ? kMoeLowTile : moe_part_rows(a.rows);
-  const Args gu{a.offsets, a.rows, a.E, a.h, a.d, a.act, static_cast<bf16*>(a.v), a.part, part_n, a.ctr, a.err};
-  cudaError_t e = launch_pair<false, kLow, false>(gu, tm_g, tm_u, tm_x, tm_x16, s);
-  if (e != cudaSuccess) return e;
-  const Args dn{a.offsets, a.rows, a.E,    a.d,    a.h, a.act, static_cast<bf16*>(a.ys), a.part,
-                part_n,    a.ctr + 2 * kMoeMaxPairs, a.err};
-  if constexpr (!kLow) {
-    // Half as many tiles twice as wide, as long as they go round half the pairs when the rows spread
-    // over the experts.  8 experts, d 4096, h 14336: 256 rows 459 us (256 columns: 499), 8192 rows
-    // 2073 (2335); 16 wide tiles (8 experts of 128 rows, d 1024, h 1024) 41 us (37).
-    const int spread = a.E < a.rows ? a.E : a.rows, high = (a.rows + kMoeTileRows - 1) / kMoeTileRows;
-    if ((long long)(spread > high ? spread : high) * ((a.d + 511) / 512) * 4 >= sm_count()) return launch_pair<true, false, true>(dn, tm_d, tm_d, tm_v, tm_v16, s);
-  }
-  return launch_pair<true, kLow, false>(dn, tm_d, tm_d, tm_v, tm_v16, s);
+  return cudaLaunchKernelEx(&cfg, pair_kernel<kDown, kWide>, p, w0, w1, r64, r16);
 }
 
 }  // namespace
 
 cudaError_t launch_moe_ffn(const MoeFfnArgs& a, cudaStream_t s) {
-  return moe_low(a.rows, a.E) ? launch_ffn<true>(a, s) : launch_ffn<false>(a, s);
+  if (moe_low(a.rows, a.E)) return launch_moe_ffn_low(a, s);
+  CUtensorMap tm_g, tm_u, tm_x64, tm_x16, tm_d, tm_v64, tm_v16;
+  if (!encode_weights(&tm_g, a.W_gate, a, 128) || !encode_weights(&tm_u, a.W_up, a, 128) ||
+      !encode_weights(&tm_d, a.W_down_t, a, 64) || !encode_rows(&tm_x64, a.xs, a.rows, a.d, 64) ||
+      !encode_rows(&tm_x16, a.xs, a.rows, a.d, 16) || !encode_rows(&tm_v64, a.v, a.rows, a.h, 64) ||
+      !encode_rows(&tm_v16, a.v, a.rows, a.h, 16))
+    return cudaErrorInvalidValue;
+  const int part_n = moe_part_rows(a.rows);
+  const Args gu{a.offsets, a.rows, a.E, a.h, a.d, a.act, static_cast<bf16*>(a.v), a.part, part_n, a.ctr, a.err};
+  cudaError_t e = launch_pair<false, false>(gu, tm_g, tm_u, tm_x64, tm_x16, s);
+  if (e != cudaSuccess) return e;
+  const Args dn{a.offsets, a.rows, a.E,    a.d,    a.h, a.act, static_cast<bf16*>(a.ys), a.part,
+                part_n,    a.ctr + 2 * kMoeMaxPairs, a.err};
+  // Half as many tiles twice as wide, as long as they go round half the pairs when the rows spread
+  // over the experts.  8 experts, d 4096, h 14336: 256 rows 459 us (256 columns: 499), 8192 rows 2073
+  // (2335); 16 wide tiles (8 experts of 128 rows, d 1024, h 1024) 41 us (37).
+  const int spread = a.E < a.rows ? a.E : a.rows, high = (a.rows + kMoeTileRows - 1) / kMoeTileRows;
+  const long long wide = (long long)(spread > high ? spread : high) * ((a.d + 511) / 512);
+  return wide * 4 >= sm_count() ? launch_pair<true, true>(dn, tm_d, tm_d, tm_v64, tm_v16, s)
+                                : launch_pair<true, false>(dn, tm_d, tm_d, tm_v64, tm_v16, s);
 }
 
 }  // namespace csffn
