@@ -12,8 +12,8 @@ namespace moe {
 
 constexpr int kKB = 64;                            // contraction elements per stage
 constexpr uint32_t kRowBytes = kKB * 2;            // one row of a stage's tile
-constexpr int kMaxParts = 8, kMaxPartsTall = 4;    // parts of a tile
-constexpr int kMinSaved = 16, kMinSavedTall = 24;  // k-blocks
+constexpr int kMaxParts = 8, kMaxPartsTall = 4;                       // parts of a tile
+constexpr int kMinSaved = 16, kMinSavedRun = 24, kMinSavedTall = 24;  // k-blocks
 
 struct Args {
   const int32_t* offsets;
@@ -110,7 +110,7 @@ struct Items {
     // of a low tile or 20 of a tall one: cut only where that many k-blocks less are to be done.
     split = left ? min(min(pairs / left, low ? kMaxParts : kMaxPartsTall), n_kb) : 1;
     if (n_kb - n_kb / split < (low ? kMinSaved : kMinSavedTall)) split = 1;
-    if (low && left && pairs / left == 1 && n_kb - (int)((long long)n_kb * left / pairs) >= kMinSaved) split = 0;
+    if (low && left && pairs / left == 1 && n_kb - (int)((long long)n_kb * left / pairs) >= kMinSavedRun) split = 0;
     next = pair;
     it = split == 0 ? run_start(pair) : 0;
     it1 = split == 0 ? run_start(pair + 1) : 0;
