@@ -430,3 +430,97 @@ def test_stack_two_streams():
                     stack.moe_stack(blocks, h, b)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------------------------ sizes and uses at the edge
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements: the last rows are right in every row-wise operator."""
+    g = gen(21)
+    T, k, d, E = 66000, 2, 16384, 2
+    x = torch.empty(T, d, dtype=BF, device="cuda").normal_(generator=g)
+    ids = torch.stack([torch.zeros(T), torch.ones(T)], 1).to(device="cuda", dtype=I32)
+    got = run_dispatch(x, ids, E)
+    n = T * k
+    assert got["xs"].numel() > 2 ** 31 and got["offsets"].tolist() == [0, T, n]
+    for p in (0, T - 1, T, n - 2, n - 1):
+        assert torch.equal(got["xs"][p], x[p % T])
+    layer = make_experts(g, E, d, 8)
+    ys = torch.zeros_like(got["xs"])
+    ws = cs.new_moe_workspace(layer, n)
+    cs.moe_ffn_forward(layer, got["xs"], got["offsets"], ys, ws)
+    assert cs.check_status(ws) == 0
+    last = slice(n - 70, n)
+    want, size = oracle.moe_ffn(np64(got["xs"][last]), [0, 0, 70], np64(layer.w_gate), np64(layer.w_up), np64(layer.w_down_t), "silu")
+    within(np64(ys[last]), want, U16 * (size + np.abs(want)) + 2.0 ** -10 * size)
+    del x
+    w = torch.rand(T, k, generator=g, device="cuda")
+    out = torch.empty(T, d, device="cuda")
+    cs.moe_combine(ys, got["pos"], w, out)
+    t = slice(T - 3, T)
+    y2 = torch.stack([ys[T - 3:T], ys[n - 3:n]], 1)
+    want = (np64(y2) * np64(w[t])[:, :, None]).sum(1)
+    within(np64(out[t]), want, (k + 2) * U32 * (np.abs(np64(y2)) * np64(w[t])[:, :, None]).sum(1))
+    del got, out, y2
+    h = torch.empty(n, d, device="cuda").normal_(generator=g)
+    xn = torch.empty(n, d, dtype=BF, device="cuda")
+    cs.block_norm(h, ys, h, xn, out_scale=0.0, res_scale=2.0)
+    assert h.numel() > 2 ** 31
+    _, want = oracle.block_norm(np64(h[last]))
+    within(np64(xn[last]), want, 48 * U32 * np.abs(want) + U16 * 1.01 * np.abs(want))
+
+
+def test_many_tokens_router():
+    """The most tokens: projection and selection of the first and the last rows."""
+    g = gen(22)
+    T, E, d = 1 << 22, 40, 16
+    x, w = rnd(g, T, d), rnd(g, E, d)
+    lg = torch.empty(T, E, device="cuda")
+    cs.moe_logits(x, w, lg)
+    ids, wt = torch.empty(T, 1, dtype=I32, device="cuda"), torch.empty(T, 1, device="cuda")
+    cs.moe_route(lg, ids, wt)
+    for t in (slice(0, 200), slice(T - 200, T)):
+        want = oracle.moe_logits(np64(x[t]), np64(w))
+        within(np64(lg[t]), want, (d / 16 + 16) * 2.0 ** -23 * (np.abs(np64(x[t])) @ np.abs(np64(w)).T))
+        assert torch.equal(ids[t, 0].long(), lg[t].argmax(1)) and (wt[t] == 1).all()
+    offsets, order = torch.empty(E + 1, dtype=I32, device="cuda"), torch.empty(T, dtype=I32, device="cuda")
+    pos, xs = torch.empty(T, 1, dtype=I32, device="cuda"), torch.empty(T, d, dtype=BF, device="cuda")
+    cs.moe_dispatch(x, ids, offsets, order, pos, xs, cs.new_moe_dispatch_workspace(T, E))
+    want = torch.sort(ids[:, 0], stable=True).indices
+    assert torch.equal(order.long(), want) and torch.equal(xs, x[want])
+    assert torch.equal(offsets[1:].long(), torch.cumsum(torch.bincount(ids[:, 0], minlength=E), 0))
+
+
+def test_layer_in_a_graph_between_eager_calls():
+    """One workspace for a captured layer and for eager calls of other row counts, in turn on one stream."""
+    g = gen(23)
+    layer = make_experts(g, 8, 256, 512)
+    ws = cs.new_moe_workspace(layer, 600)
+    xs = rnd(g, 600, 256)
+    off = {n: torch.tensor([n * i // 8 for i in range(9)], dtype=I32, device="cuda") for n in (24, 600)}
+    ys = torch.zeros(600, 256, dtype=BF, device="cuda")
+    want = {}
+    for n in (24, 600):
+        cs.moe_ffn_forward(layer, xs[:n], off[n], ys[:n], ws)
+        want[n] = ys[:n].clone()
+    graph = torch.cuda.CUDAGraph()
+    yg = torch.zeros(24, 256, dtype=BF, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        cs.moe_ffn_forward(layer, xs[:24], off[24], yg, ws)
+    for _ in range(3):
+        yg.zero_()
+        ys.zero_()
+        cs.moe_ffn_forward(layer, xs, off[600], ys, ws)
+        graph.replay()
+        assert torch.equal(yg, want[24]) and torch.equal(ys, want[600])
+    assert cs.check_status(ws) == 0
+
+
+def test_workspace_too_small_for_the_rows():
+    layer = make_experts(gen(24), 4, 64, 64)
+    ws = cs.new_moe_dispatch_workspace(64, 4)
+    xs = torch.zeros(64, 64, dtype=BF, device="cuda")
+    with pytest.raises(cs.CsffnError) as e:
+        cs.moe_ffn_forward(layer, xs, torch.zeros(5, dtype=I32, device="cuda"), xs.clone(), ws)
+    assert e.value.status == _abi.ERR_WORKSPACE
