@@ -155,6 +155,25 @@ def test_dispatch(T, E, k, d, drop, dtype):
     check_dispatch(x, ids, E, run_dispatch(x, ids, E))
 
 
+@pytest.mark.parametrize("T,k", [(1023, 1), (1024, 1), (1025, 1), (341, 3), (2048, 8), (16385, 1), (1023, 16), (8192, 8),
+                                 (16384, 16), (16385, 16), (131072, 2)])
+def test_dispatch_sizes_of_its_forms(T, k):
+    """Slot counts around those where one kernel, one cluster or many CTAs plan the sort."""
+    g = gen(T + k)
+    x, ids = rnd(g, T, 16), random_ids(g, T, 37, k, 0.05)
+    got = run_dispatch(x, ids, 37)
+    flat = ids.reshape(-1).long()
+    key = torch.where(flat < 0, 37, flat)
+    want = torch.sort(key, stable=True).indices
+    n = int((flat >= 0).sum())
+    assert torch.equal(got["order"][:n].long(), want[:n]) and (got["order"][n:] == -9).all()
+    assert got["offsets"].tolist() == [int((key < e).sum()) for e in range(38)]
+    pos = torch.full_like(flat, -1)
+    pos[want[:n]] = torch.arange(n, device="cuda")
+    assert torch.equal(got["pos"].reshape(-1).long(), pos)
+    assert torch.equal(got["xs"][:n], x[want[:n] // k]) and (got["xs"][n:] == 7.0).all()
+
+
 def test_dispatch_one_expert_takes_all():
     x, ids = rnd(gen(1), 2000, 32), torch.full((2000, 2), 5, dtype=I32, device="cuda")
     check_dispatch(x, ids, 9, run_dispatch(x, ids, 9))
