@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(kThreads)
       __syncwarp();
       tmem_ld16(acc + (uint32_t)c, a);
       tmem_ld16(acc + (uint32_t)(kMaxN + c), b);
-      tmem_ld_wait();
+      tmem_ld_wait(a);
+      tmem_ld_wait(b);
       if (s_err) {  // a wait ran out: no logits
 #pragma unroll
         for (int k = 0; k < 16; ++k) a[k] = __int_as_float(0x7fc00000);
