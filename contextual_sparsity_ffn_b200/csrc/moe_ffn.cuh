@@ -71,6 +71,7 @@ struct Tile {
   int e, m;        // expert, output block
   int row0, row1;  // rows
   int n;           // N of its MMAs: the rows rounded up to 32
+  bool once;       // no other tile reads its weights
 };
 
 __device__ __forceinline__ Tile find_tile(const Plan& p, int E, int mb, int i) {
@@ -92,6 +93,7 @@ __device__ __forceinline__ Tile find_tile(const Plan& p, int E, int mb, int i) {
   t.row0 = p.lo[a] + (r % nt) * height;
   t.row1 = min(t.row0 + height, p.lo[a + 1]);
   t.n = (t.row1 - t.row0 + 31) / 32 * 32;
+  t.once = nt == 1;
   return t;
 }
 

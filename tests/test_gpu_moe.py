@@ -251,7 +251,8 @@ def test_ffn(d, h, counts, spare, act):
 @pytest.mark.parametrize("d,h,counts", [
     (4096, 512, [40]), (4096, 512, [300, 40]), (1024, 4096, [5, 0, 9]), (4096, 2560, [2, 1, 30, 0, 8, 4]),
     (2048, 4104, [33, 1]), (512, 2048, [600, 900, 10, 1300]), (1032, 264, [70, 3, 0, 300, 1, 8, 257, 31, 64, 5, 9, 2, 128, 40]),
-    (264, 520, [10 + 3 * i for i in range(45)]), (8200, 128, [90, 200, 33]), (64, 8200, [400])])
+    (264, 520, [10 + 3 * i for i in range(45)]), (8200, 128, [90, 200, 33]), (64, 8200, [400]),
+    (4096, 5376, [3]), (10240, 3584, [7])])
 def test_ffn_split_tiles(d, h, counts):
     g = gen(d + h)
     check_ffn(make_experts(g, len(counts), d, h), rnd(g, sum(counts), d), counts)
