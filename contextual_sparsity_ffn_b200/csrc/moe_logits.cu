@@ -15,6 +15,10 @@
 // reads its share of the weights, as many bytes as of x) and the cluster's sum are the rest.  Every
 // wait is bounded (one second); there is no workspace to record one that ran out, so its tile's
 // logits become NaN.
+//
+// Both kernels read the router weights after the dependency wait only, as they do x: the weights may
+// be another call's output (a router normalised per call by csffn_block_norm), and that kernel, or a
+// chained one after it, has let this one start before the weights were complete.
 #include "common.cuh"
 #include "kernels.h"
 #include "tcgen05.cuh"
@@ -26,8 +30,8 @@ namespace {
 
 constexpr int kRowThreads = 256, kRowTokens = 8;
 
-__global__ void __launch_bounds__(kRowThreads) row_kernel(const bf16* __restrict__ x, const bf16* __restrict__ w, int T,
-                                                          int E, int d, float* __restrict__ logits) {
+__global__ void __launch_bounds__(kRowThreads) row_kernel(const bf16* x, const bf16* w, int T, int E, int d,
+                                                          float* logits) {
   __shared__ float part[kRowThreads / kWarp][kRowTokens];
   pdl_trigger();
   const int e = blockIdx.x, t0 = blockIdx.y * kRowTokens, n = min(kRowTokens, T - t0);
@@ -36,11 +40,11 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const bf16* __restrict
   const uint4* xr = reinterpret_cast<const uint4*>(x) + (size_t)t0 * vecs;
   float acc[kRowTokens] = {};
   uint4 wv = make_uint4(0u, 0u, 0u, 0u);
-  if ((int)threadIdx.x < vecs) wv = wr[threadIdx.x];
   pdl_wait_prior();
+  if ((int)threadIdx.x < vecs) wv = __ldcg(wr + threadIdx.x);
   for (int v = threadIdx.x; v < vecs; v += kRowThreads) {
     const uint4 cur = wv;
-    if (v + kRowThreads < vecs) wv = wr[v + kRowThreads];
+    if (v + kRowThreads < vecs) wv = __ldcg(wr + v + kRowThreads);
     uint4 xv[kRowTokens];
 #pragma unroll
     for (int t = 0; t < kRowTokens; ++t)
@@ -92,7 +96,7 @@ __device__ __forceinline__ float4 load_cluster(uint32_t addr) {
 }
 
 __global__ void __launch_bounds__(kThreads)
-    tile_kernel(int T, int E, int d, float* __restrict__ logits, int split,
+    tile_kernel(int T, int E, int d, float* logits, int split,
                 const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w) {
   extern __shared__ __align__(1024) unsigned char lg_raw[];
   __shared__ __align__(8) uint64_t full[kStages], empty[kStages], accf;
@@ -125,25 +129,20 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
+  // Before anything is read (and written: the logits may still be read by what came before), and before
+  // a bounded wait could count the time of the kernels before this one.
+  pdl_wait_prior();
 
   if (warp == 0) {
     if (lane == 0) {
-      // ---- producer: the first stages' weights before the dependency wait
-      const int pre = min(kStages, kb1 - kb0);
-      for (int q = 0; q < pre; ++q) {
-        mbar_arrive_expect_tx(&full[q], kStage);
-        tma_load_2d_plain(smem + (size_t)q * kStage + kXBytes, &tm_w, (kb0 + q) * kKB, e0, &full[q]);
-      }
-      pdl_wait_prior();
+      // ---- producer
       int issued = 0;
       for (int kb = kb0; kb < kb1; ++kb, ++issued) {
         const int slot = issued % kStages;
         unsigned char* st = smem + (size_t)slot * kStage;
-        if (issued >= pre) {
-          if (!mbar_wait(&empty[slot], (uint32_t)(issued / kStages - 1) & 1, &s_err, &s_abort)) break;
-          mbar_arrive_expect_tx(&full[slot], kStage);
-          tma_load_2d_plain(st + kXBytes, &tm_w, kb * kKB, e0, &full[slot]);
-        }
+        if (issued >= kStages && !mbar_wait(&empty[slot], (uint32_t)(issued / kStages - 1) & 1, &s_err, &s_abort)) break;
+        mbar_arrive_expect_tx(&full[slot], kStage);
+        tma_load_2d_plain(st + kXBytes, &tm_w, kb * kKB, e0, &full[slot]);
         tma_load_2d_plain(st, &tm_x, kb * kKB, t0, &full[slot]);
       }
       for (int q = issued > kStages ? issued - kStages : 0; q < issued; ++q)
@@ -198,7 +197,6 @@ __global__ void __launch_bounds__(kThreads)
     tc_fence_after();
     tmem_dealloc(tmem, 2 * kMaxN);
   }
-  pdl_wait_prior();  // the logits may still be read by what came before
   // this CTA's share of the tokens
   const int r0 = rank * kM / split, r1 = (rank + 1) * kM / split, vecs = n / 4, width = min(kMaxN, E - e0);
   uint32_t base[kMaxSplit];

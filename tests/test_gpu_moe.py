@@ -544,3 +544,32 @@ def test_workspace_too_small_for_the_rows():
     with pytest.raises(cs.CsffnError) as e:
         cs.moe_ffn_forward(layer, xs, torch.zeros(5, dtype=I32, device="cuda"), xs.clone(), ws)
     assert e.value.status == _abi.ERR_WORKSPACE
+
+
+# ------------------------------------------------------------------------------ weights made in the stream
+
+@pytest.mark.parametrize("chained", [False, True])
+@pytest.mark.parametrize("T,E,d", [(4, 64, 2048), (4, 512, 16384), (256, 128, 8192), (256, 512, 4096)])
+def test_logits_of_weights_made_just_before(T, E, d, chained):
+    """A router whose weights block_norm makes in the stream just before the projection, with and without
+    a chained kernel between the two: the projection sees all of them.  Replayed, so that the kernels
+    follow one another without a gap, on weights that are NaN until they are made."""
+    g = gen(E + T)
+    x, w32 = rnd(g, T, d), rnd(g, E, d, dtype=F32)
+    w16, want, out = torch.empty(E, d, dtype=BF, device="cuda"), torch.empty(T, E, device="cuda"), torch.empty(T, E, device="cuda")
+    cs.block_norm(w32, None, None, w16)
+    torch.cuda.synchronize()
+    cs.moe_logits(x, w16, want)
+    lg, ids, wt = rnd(g, 8, 16, dtype=F32), torch.empty(8, 2, dtype=I32, device="cuda"), torch.empty(8, 2, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        w16.fill_(float("nan"))
+        cs.block_norm(w32, None, None, w16)
+        if chained:
+            cs.moe_route(lg, ids, wt)
+        cs.moe_logits(x, w16, out)
+    for _ in range(5):
+        out.fill_(float("nan"))
+        graph.replay()
+        assert torch.equal(out, want)
