@@ -30,6 +30,10 @@ constexpr int kN = kMoeLowTile;                       // rows per tile
 constexpr uint32_t kWBytes = 128 * kRowBytes;         // weights of a stage: 16 KB
 constexpr uint32_t kRowsBytes = kN * kRowBytes;       // rows of a stage (of one part of v): 4 KB
 
+// What rounding v to its high part left.  Nothing where the high part is infinite: v itself, or a v
+// past bf16's range; inf - inf would make the row NaN.
+__device__ __forceinline__ float rest(float v, float high) { return fabsf(high) < INFINITY ? v - high : 0.f; }
+
 template <bool kDown>
 struct Cfg {
   static constexpr int kTileOut = kDown ? 128 : 64;
@@ -274,8 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < 8; ++k) {
           const __nv_bfloat162 v = __floats2bfloat162_rn(g[2 * k], g[2 * k + 1]);
           p[k] = reinterpret_cast<const uint32_t&>(v);
-          g[2 * k] -= bf16lo(p[k]);
-          g[2 * k + 1] -= bf16hi(p[k]);
+          g[2 * k] = rest(g[2 * k], bf16lo(p[k]));
+          g[2 * k + 1] = rest(g[2 * k + 1], bf16hi(p[k]));
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {

@@ -573,3 +573,37 @@ def test_logits_of_weights_made_just_before(T, E, d, chained):
         out.fill_(float("nan"))
         graph.replay()
         assert torch.equal(out, want)
+
+
+# ------------------------------------------------------------------------------ values past the range of bf16
+
+@pytest.mark.parametrize("act", ["silu", "relu"])
+@pytest.mark.parametrize("rows", [3, 64, 65, 300])
+def test_ffn_overflowing_row(rows, act):
+    """One neuron of one row overflows (in fp32, or only when it is rounded to bf16): that row is +-inf by
+    the signs of the neuron's down weights, with few rows and with many, and the other rows keep their bits."""
+    g = gen(rows)
+    d, h = 72, 136
+    wg, wu, wd = (rnd(g, 1, h, d, std=s) for s in (d ** -0.5, d ** -0.5, h ** -0.5))
+    wg[0, :, :2] = wu[0, :, :2] = 0
+    wg[0, 5], wu[0, 5] = 0, 0
+    wg[0, 5, 0] = wu[0, 5, 1] = 1  # neuron 5: z = x[0], u = x[1]
+    wd[0, 5] = torch.where(wd[0, 5] == 0, torch.ones_like(wd[0, 5]), wd[0, 5])
+    layer = cs.MoELayer(wg, wu, wd, _abi.ACT_SILU if act == "silu" else _abi.ACT_RELU)
+    xs = rnd(g, rows, d)
+    xs[:, :2] = 0
+    offsets = torch.tensor([0, rows], dtype=I32, device="cuda")
+    ws = cs.new_moe_workspace(layer, rows)
+    clean = torch.zeros(rows, d, dtype=BF, device="cuda")
+    cs.moe_ffn_forward(layer, xs, offsets, clean, ws)
+    edge = 181 / 128  # its square, times 2^127, is below fp32's largest value and rounds past bf16's
+    for z, u in ((1e20, 1e25), (1e20, -1e25), (edge * 2.0 ** 63, edge * 2.0 ** 64)):
+        bad = xs.clone()
+        bad[1, 0], bad[1, 1] = z, u
+        ys = torch.zeros_like(clean)
+        cs.moe_ffn_forward(layer, bad, offsets, ys, ws)
+        assert cs.check_status(ws) == 0
+        want = torch.where((wd[0, 5] > 0) == (u > 0), float("inf"), float("-inf")).to(BF)
+        assert torch.equal(ys[1], want)
+        keep = [r for r in range(rows) if r != 1]
+        assert torch.equal(ys[keep], clean[keep])
