@@ -141,7 +141,7 @@ class MoEBlock:
 
 @dataclass
 class MoEBuffers:
-    """Device buffers of routed layers of one shape for T tokens."""
+    """Device buffers of routed layers of one shape for T tokens (T may be 0)."""
 
     xn: torch.Tensor        # bf16 [T, d]: the layer's input
     logits: torch.Tensor    # fp32 [T, n_experts]
@@ -166,7 +166,7 @@ class MoEBuffers:
                    ids=empty(T, k, dtype=i32), weights=empty(T, k, dtype=torch.float32),
                    offsets=empty(L.n_experts + 1, dtype=i32), order=empty(T * k, dtype=i32), pos=empty(T, k, dtype=i32),
                    xs=empty(T * k, L.d, dtype=bf), ys=empty(T * k, L.d, dtype=bf), y=empty(T, L.d, dtype=bf),
-                   ws=cs.new_moe_workspace(L, T * k))
+                   ws=cs.new_moe_workspace(L, max(1, T * k)))  # an empty batch takes the least
 
 
 def moe_layer(block: MoEBlock, x: torch.Tensor, y: torch.Tensor, buf: MoEBuffers) -> None:

@@ -607,3 +607,24 @@ def test_ffn_overflowing_row(rows, act):
         assert torch.equal(ys[1], want)
         keep = [r for r in range(rows) if r != 1]
         assert torch.equal(ys[keep], clean[keep])
+
+
+# ------------------------------------------------------------------------------ no tokens
+
+def test_stack_of_no_tokens():
+    """An empty batch goes through the layer and the stack as it goes through every call, captured too."""
+    g = gen(31)
+    blocks = stack_blocks(g, 8, 64, 64, 2)
+    buf = stack.MoEBuffers.new(blocks[0], 0)
+    h = torch.empty(0, 64, device="cuda")
+    buf.offsets.fill_(-1)
+    stack.moe_layer(blocks[0], buf.xn, buf.y, buf)
+    assert (buf.offsets == 0).all()
+    stack.moe_stack(blocks, h, buf)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        stack.moe_stack(blocks, h, buf)
+    buf.offsets.fill_(-1)
+    graph.replay()
+    assert (buf.offsets == 0).all() and cs.check_status(buf.ws) == 0
