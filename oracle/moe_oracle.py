@@ -92,3 +92,39 @@ def block_norm(h: np.ndarray, y=None, g_post=None, gate=None, g_pre=None, res_sc
         u = y if g_post is None else rms(y) * g_post
         hn = hn + out_scale * (u if gate is None else gate * u)
     return hn, rms(hn) * (1.0 if g_pre is None else g_pre)
+
+
+def moe_ffn_parts(xs: np.ndarray, offsets, w_gate: np.ndarray, w_up: np.ndarray, act: str) -> tuple:
+    """(v, slip) on the sorted rows: v[p, i] = act(z) u, and how far v in fp32 may be from it.  An MMA adds
+    16 products and may cut the running sum by an fp32 step of 2^-23, so z and u are off by at most
+    (d / 16 + 16) 2^-23 of their sums of absolute products; the activation's slope is at most 1.1, its own
+    error (|z| + 8) 2^-22 relative (the rounded exponent, the approximate exponential and reciprocal), the
+    product's 2^-23."""
+    E, h, d = w_gate.shape
+    v, slip = np.zeros((xs.shape[0], h)), np.zeros((xs.shape[0], h))
+    for e in range(E):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        if hi > lo:
+            x, step = xs[lo:hi], (d / 16 + 16) * 2.0 ** -23
+            z, u = x @ w_gate[e].T, x @ w_up[e].T
+            dz, du = step * (np.abs(x) @ np.abs(w_gate[e]).T), step * (np.abs(x) @ np.abs(w_up[e]).T)
+            a = z / (1.0 + np.exp(-np.clip(z, -700, None))) if act == "silu" else np.maximum(z, 0.0)
+            v[lo:hi] = a * u
+            da = 1.1 * dz + (np.abs(z) + 8) * 2.0 ** -22 * np.abs(a)
+            slip[lo:hi] = da * (np.abs(u) + du) + np.abs(a) * du + 2.0 ** -23 * np.abs(a * u)
+    return v, slip
+
+
+def moe_ffn_tol_two_parts(v: np.ndarray, slip: np.ndarray, offsets, w_down_t: np.ndarray, want: np.ndarray) -> np.ndarray:
+    """How far ys may be from `want` where v reaches the down product as a bf16 high part and a bf16 low
+    part: each rounding is off by at most 2^-8 of what it rounds, so both together leave 2^-16 of v; the sum
+    over h neurons of two parts in fp32 is off by (h / 8 + 32) 2^-23 of its absolute products; ys is rounded
+    once, by 2^-8 of itself."""
+    E, h, _ = w_down_t.shape
+    b = np.zeros(want.shape)
+    for e in range(E):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        if hi > lo:
+            off = slip[lo:hi] * (1 + 2.0 ** -16) + (2.0 ** -16 + (h / 8 + 32) * 2.0 ** -23) * np.abs(v[lo:hi])
+            b[lo:hi] = off @ np.abs(w_down_t[e])
+    return b + 2.0 ** -8 * (np.abs(want) + b)

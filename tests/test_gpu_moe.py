@@ -628,3 +628,41 @@ def test_stack_of_no_tokens():
     buf.offsets.fill_(-1)
     graph.replay()
     assert (buf.offsets == 0).all() and cs.check_status(buf.ws) == 0
+
+
+# ------------------------------------------------------------------------------ the two parts of v
+
+@pytest.mark.parametrize("act", ["silu", "relu"])
+@pytest.mark.parametrize("d,h,counts,spare", [
+    (64, 64, [20, 44], 0), (72, 136, [3, 5, 0, 30], 2), (256, 200, [0, 31, 33], 0), (64, 2048, [40], 0), (64, 64, [1] * 40, 7),
+    (64, 64, [0] * 20 + [70, 0, 9], 1), (128, 1000, [33, 0, 7], 24), (264, 72, [1], 0), (1032, 64, [8] * 8, 0)])
+def test_ffn_few_rows_keep_both_parts_of_v(d, h, counts, spare, act):
+    """Up to max(64, 4 n_experts) rows v reaches the down product as a high and a low part: the tolerance
+    has no bf16 rounding of v in it, and does not hold without the low part."""
+    g = gen(d + h)
+    n = sum(counts)
+    assert n + spare <= max(64, 4 * len(counts))
+    layer = make_experts(g, len(counts), d, h, act)
+    xs = rnd(g, n, d)
+    ys = check_ffn(layer, xs, counts, act, spare)
+    off = np.concatenate([[0], np.cumsum(counts)])
+    wg, wu, wd = np64(layer.w_gate), np64(layer.w_up), np64(layer.w_down_t)
+    v, slip = oracle.moe_ffn_parts(np64(xs), off, wg, wu, act)
+    want, _ = oracle.moe_ffn(np64(xs), off, wg, wu, wd, act)
+    within(np64(ys[:n]), want, oracle.moe_ffn_tol_two_parts(v, slip, off, wd, want))
+
+
+@pytest.mark.parametrize("E,rows", [(1, 64), (1, 65), (16, 64), (16, 65), (17, 68), (17, 69), (40, 160), (40, 161)])
+def test_ffn_around_the_limit_of_few_rows(E, rows):
+    """Row counts at the limit and one above it."""
+    g = gen(E + rows)
+    counts = [rows // E + (1 if e < rows % E else 0) for e in range(E)]
+    layer = make_experts(g, E, 64, 64)
+    xs = rnd(g, rows, 64)
+    ys = check_ffn(layer, xs, counts)
+    if rows <= max(64, 4 * E):
+        off = np.concatenate([[0], np.cumsum(counts)])
+        wd = np64(layer.w_down_t)
+        v, slip = oracle.moe_ffn_parts(np64(xs), off, np64(layer.w_gate), np64(layer.w_up), "silu")
+        want, _ = oracle.moe_ffn(np64(xs), off, np64(layer.w_gate), np64(layer.w_up), wd, "silu")
+        within(np64(ys), want, oracle.moe_ffn_tol_two_parts(v, slip, off, wd, want))

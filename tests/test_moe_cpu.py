@@ -61,6 +61,34 @@ def test_ffn_combine_norm_by_hand():
     np.testing.assert_allclose(xn, hn / np.sqrt((49 + 64) / 2))
 
 
+def bf16(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(torch.bfloat16).double().numpy()
+
+
+@pytest.mark.parametrize("act", ["silu", "relu"])
+@pytest.mark.parametrize("d,h,counts", [(64, 64, [20, 44]), (72, 136, [3, 5, 0, 30]), (256, 200, [0, 31, 33]),
+                                        (64, 2048, [40]), (64, 64, [1] * 40)])
+def test_two_part_tolerance_sees_a_lost_part(d, h, counts, act):
+    """The tolerance of a v in two bf16 parts holds for such a v, and does not hold when the low part is
+    lost, taken from the row before, or added twice."""
+    rng = np.random.default_rng(d + h)
+    off = np.concatenate([[0], np.cumsum(counts)])
+    E, n = len(counts), off[-1]
+    xs, wg, wu, wd = (bf16(rng.standard_normal(s) * f) for s, f in (((n, d), 1), ((E, h, d), d ** -0.5), ((E, h, d), d ** -0.5),
+                                                                    ((E, h, d), h ** -0.5)))
+    v, slip = oracle.moe_ffn_parts(xs, off, wg, wu, act)
+    want, _ = oracle.moe_ffn(xs, off, wg, wu, wd, act)
+    tol = oracle.moe_ffn_tol_two_parts(v, slip, off, wd, want)
+    high = bf16(v)
+    low = bf16(v - high)
+
+    def outside(p):
+        ys = bf16(np.concatenate([p[off[e]:off[e + 1]] @ wd[e] for e in range(E)]))
+        return int((~(np.abs(ys - want) <= tol)).sum())
+    assert outside(high + low) == 0
+    assert min(outside(high), outside(high + np.roll(low, 1, axis=0)), outside(high + 2 * low)) > 0
+
+
 # ------------------------------------------------------------------------------ refusals of the C ABI
 
 def moe_layer(d=256, h=128, E=4, act=_abi.ACT_SILU, w=FAKE):
