@@ -39,6 +39,16 @@ inline csffn_status cuda_status(cudaError_t e) { return e == cudaSuccess ? CSFFN
 template <typename T>
 T* at(void* ws, size_t off) { return reinterpret_cast<T*>(reinterpret_cast<char*>(ws) + off); }
 
+// Whether two buffers share a byte.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return x < y + b.bytes && y < x + a.bytes;
+}
+
 csffn_status check_width(int d) {
   if (d < 8 || d > CSFFN_MAX_D) return CSFFN_ERR_UNSUPPORTED_SHAPE;
   return d % 8 ? CSFFN_ERR_ALIGNMENT : CSFFN_OK;
@@ -114,6 +124,16 @@ csffn_status csffn_moe_dispatch(const void* x, int xdtype, const int32_t* ids, i
     return CSFFN_ERR_ALIGNMENT;
   const MoeWs L = moe_ws_layout(T * k, E, 0);
   if (!ws || ws_bytes < L.total || !aligned16(ws)) return CSFFN_ERR_WORKSPACE;
+  // The CTAs write while others still read, so no output may lie on an input, or on another output:
+  // pos in the place of ids, of the same shape and type, is the one that invites it.
+  const size_t R = (size_t)T * k, row = (size_t)d * (xdtype == CSFFN_BF16 ? 2 : 4);
+  const Span in[2] = {{x, T * row}, {ids, 4 * R}};
+  const Span out[4] = {{offsets, 4 * ((size_t)E + 1)}, {order, 4 * R}, {pos, 4 * R}, {xs, R * row}};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return CSFFN_ERR_INVALID_ARG;
+    if (overlap(out[i], in[0]) || overlap(out[i], in[1])) return CSFFN_ERR_INVALID_ARG;
+  }
   DispatchArgs a{};
   a.x = x;
   a.ids = ids;

@@ -129,6 +129,28 @@ def test_dispatch_refusals(lib):
     assert lib.csffn_moe_dispatch_workspace_size((1 << 22) + 1, 8) == lib.csffn_moe_dispatch_workspace_size(8, 513) == 0
 
 
+def test_dispatch_refuses_overlapping_buffers(lib):
+    """T = 4, k = 2, E = 8, rows of 512 bytes: every buffer at an address of its own, then one output moved
+    onto another buffer, onto its last word, or to where the two share one word."""
+    size = dict(x=4 * 512, ids=32, off=36, order=32, pos=32, xs=8 * 512)
+    base = {n: FAKE + 0x10000 * i for i, n in enumerate(size)}
+
+    def f(n=BIG, **at):
+        p = {**base, **at}
+        return lib.csffn_moe_dispatch(p["x"], _abi.BF16, p["ids"], 4, 2, 8, 256, p["off"], p["order"], p["pos"], p["xs"],
+                                      FAKE, n, None)
+    assert f(n=8) == WS
+    for a, b in (("pos", "ids"), ("order", "ids"), ("off", "ids"), ("xs", "ids"), ("xs", "x"), ("pos", "x"), ("order", "x"),
+                 ("off", "x"), ("order", "off"), ("pos", "off"), ("pos", "order"), ("xs", "order"), ("xs", "pos"), ("xs", "off")):
+        assert f(**{a: base[b]}) == ARG
+        last = base[b] + size[b] - 4
+        if a != "xs" or last % 16 == 0:
+            assert f(**{a: last}) == ARG
+        below = base[b] - size[a] + 4
+        if a != "xs" or below % 16 == 0:
+            assert f(**{a: below}) == ARG
+
+
 def test_ffn_refusals(lib):
     def f(L=None, xs=FAKE, off=FAKE, rows=8, ys=FAKE + 0x10000, ws=FAKE, n=BIG):
         L = moe_layer() if L is None else L
