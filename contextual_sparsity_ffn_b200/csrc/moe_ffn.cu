@@ -136,9 +136,12 @@ __global__ void __launch_bounds__(Cfg<kDown, kWide>::kThreads, 1)
   }
   // The gate/up kernel lets the down kernel start only after its own wait, so what came before the
   // gate/up kernel is complete when the down kernel starts: the offsets (and the weights) may be read
-  // before the down kernel's wait, v after it.
-  if (!kDown) pdl_wait_prior();
-  pdl_trigger();
+  // before the down kernel's wait, v after it.  The down kernel lets nothing start early: ys may be weights
+  // of the call that follows.
+  if (!kDown) {
+    pdl_wait_prior();
+    pdl_trigger();
+  }
   for (int e = threadIdx.x; e <= a.E; e += C::kThreads) s_plan.lo[e] = __ldcg(a.offsets + e);
   tc_fence_before();
   __syncthreads();

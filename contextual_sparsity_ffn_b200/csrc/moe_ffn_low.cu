@@ -84,9 +84,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   // As in moe_ffn.cu: the down kernel starts after the gate/up kernel's wait, so it may read the offsets
-  // and the weights before its own, and v after it.
-  if (!kDown) pdl_wait_prior();
-  pdl_trigger();
+  // and the weights before its own, and v after it; and it lets nothing start early.
+  if (!kDown) {
+    pdl_wait_prior();
+    pdl_trigger();
+  }
   for (int e = threadIdx.x; e <= a.E; e += kThreads) s_plan.lo[e] = __ldcg(a.offsets + e);
   __syncthreads();
   if (warp == 0) make_plan<kN>(a, &s_plan);

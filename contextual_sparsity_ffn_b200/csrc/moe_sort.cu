@@ -14,6 +14,10 @@
 // 64 experts, d 2048 bf16: the three kernels 53 us, of which the gather is 43 (41 at the copy rate);
 // 13 tokens in the one kernel: 4.5 us, the latency of its chain of loads, counts and stores.
 //
+// The kernels that write rows (xs, out) do not let the next kernel start early: the rows may be weights
+// of the call that follows (tcgen05.cuh).  It costs nothing: combine, 512 tokens, call after call 4.6 us
+// (6.2 with the trigger, whose waiting CTAs take the place of working ones).
+//
 // Combine: one pass over the tokens: each thread owns 8 columns and adds the token's k rows in slot
 // order in fp32, so the sum does not depend on timing (no atomics).  Bound by memory: the same
 // tokens 46 us (41 at the copy rate).
@@ -281,7 +285,6 @@ constexpr int kGatherThreads = 128;
 
 __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const DispatchArgs a, int per_token) {
   __shared__ int s_pos[(kGatherThreads / kWarp) * CSFFN_MAX_TOPK];
-  pdl_trigger();
   pdl_wait_prior();
   const int tokens = kGatherThreads / per_token, t0 = blockIdx.x * tokens;
   const int n = min(tokens, a.T - t0) * a.k;
@@ -298,7 +301,6 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_small_kernel(const Disp
   __shared__ int s_pos[kMoeChunk];
   int* whist = sort_smem;
   int* tot = whist + kSortWarps * a.E;
-  pdl_trigger();
   pdl_wait_prior();
   const int R = a.T * a.k, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int ex[kRounds], first;
@@ -335,7 +337,6 @@ constexpr int kCombineThreads = 128;
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineArgs a, int per_token) {
   __shared__ int s_pos[(kCombineThreads / kWarp) * CSFFN_MAX_TOPK];
   __shared__ float s_w[(kCombineThreads / kWarp) * CSFFN_MAX_TOPK];
-  pdl_trigger();
   pdl_wait_prior();
   const int tokens = kCombineThreads / per_token, t0 = blockIdx.x * tokens;
   const int n = min(tokens, a.T - t0) * a.k;

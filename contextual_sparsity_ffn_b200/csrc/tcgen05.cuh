@@ -262,7 +262,9 @@ __device__ __forceinline__ bool named_all(int bar, int threads, bool pred) {
 }
 
 // Programmatic dependent launch: let the next kernel in the stream start scheduling, and wait for
-// the previous kernel's completion (and its memory) before touching what it wrote.
+// the previous kernel's completion (and its memory) before touching what it wrote.  The decode steps
+// of a csffn_layer read its weights before they wait, so a kernel that writes matrices of any height,
+// which may be such weights, does not trigger: what follows it then starts when it is complete.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait_prior() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -666,3 +666,67 @@ def test_ffn_around_the_limit_of_few_rows(E, rows):
         v, slip = oracle.moe_ffn_parts(np64(xs), off, np64(layer.w_gate), np64(layer.w_up), "silu")
         want, _ = oracle.moe_ffn(np64(xs), off, np64(layer.w_gate), np64(layer.w_up), wd, "silu")
         within(np64(ys), want, oracle.moe_ffn_tol_two_parts(v, slip, off, wd, want))
+
+
+@pytest.mark.parametrize("chained", [False, True])
+@pytest.mark.parametrize("maker", ["block_norm", "dispatch", "ffn", "ffn few rows", "combine"])
+def test_ffn_layer_of_weights_made_just_before(maker, chained):
+    """The weights of a csffn_layer, whose decode steps read them before they wait, made in the stream just
+    before by the calls that write rows, with and without a chained kernel in between; replayed, on weights
+    that are NaN until they are made."""
+    g = gen(77)
+    d, h = (512, 5000) if maker != "ffn few rows" else (4096, 2048)
+    fixed = [rnd(g, h, d, std=d ** -0.5) for _ in range(3)]
+    w = torch.empty(h, d, dtype=BF, device="cuda")
+    tokens = {1: rnd(g, 1, d), 16: rnd(g, 16, d)}
+    src, src32 = rnd(g, h, d), rnd(g, h, d, dtype=F32)
+    ids = torch.zeros(h, 1, dtype=I32, device="cuda")
+    pos = torch.randperm(h, generator=g, device="cuda").to(I32)[:, None].contiguous()
+    off, order, back = (torch.empty(n, dtype=I32, device="cuda") for n in (2, h, h))
+    E = 1 if maker != "ffn few rows" else 512
+    experts = make_experts(g, E, d, 64)
+    bounds = torch.tensor([h * e // E for e in range(E + 1)], dtype=I32, device="cuda")
+    ews, dws = cs.new_moe_workspace(experts, h), cs.new_moe_dispatch_workspace(h, 1)
+
+    def make():
+        if maker == "block_norm":
+            cs.block_norm(src32, None, None, w)
+        elif maker == "dispatch":
+            cs.moe_dispatch(src, ids, off, order, back[:, None], w, dws)
+        elif maker == "combine":
+            cs.moe_combine(src, pos, None, w)
+        else:
+            cs.moe_ffn_forward(experts, src, bounds, w, ews)
+
+    lg, ri, rw = rnd(g, 8, 16, dtype=F32), torch.empty(8, 2, dtype=I32, device="cuda"), torch.empty(8, 2, device="cuda")
+    for place in range(3):  # as gate, up or down weights
+        layer = cs.FFNLayer(*[w if i == place else fixed[i] for i in range(3)], _abi.ACT_SILU)
+        buf = cs.DecodeBuffers.new(layer, 16)
+        for step in ("sparse", "dense", "verify"):
+            x = tokens[16 if step == "verify" else 1]
+            out = torch.empty(x.shape[0], d, device="cuda")
+
+            def use():
+                if step == "sparse":
+                    cs.cats_decode(layer, x, 0.05, out, buf)
+                else:
+                    cs.dense_ffn_forward(layer, x, out, buf.ws)
+            make()
+            torch.cuda.synchronize()
+            use()
+            want = out.double()
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                w.fill_(float("nan"))
+                make()
+                if chained:
+                    cs.moe_route(lg, ri, rw)
+                use()
+            for _ in range(3):
+                out.fill_(float("nan"))
+                graph.replay()
+                # the sparse step adds its kept neurons' shares in the order they come: at most h fp32
+                # additions of terms whose absolute sum is taken as 100 times the result's norm
+                assert (out.double() - want).norm() <= 100 * h * U32 * want.norm()
+            assert cs.check_status(buf.ws) == 0
