@@ -49,9 +49,9 @@ bool overlap(const Span& a, const Span& b) {
   return x < y + b.bytes && y < x + a.bytes;
 }
 
-csffn_status check_width(int d) {
+csffn_status check_width(int d, int multiple = 8) {
   if (d < 8 || d > CSFFN_MAX_D) return CSFFN_ERR_UNSUPPORTED_SHAPE;
-  return d % 8 ? CSFFN_ERR_ALIGNMENT : CSFFN_OK;
+  return d % multiple ? CSFFN_ERR_ALIGNMENT : CSFFN_OK;
 }
 
 bool known_out_mode(int m) {
@@ -115,7 +115,7 @@ csffn_status csffn_moe_dispatch(const void* x, int xdtype, const int32_t* ids, i
   if (!known_dtype(xdtype) || E < 1 || E > CSFFN_MAX_EXPERTS) return CSFFN_ERR_INVALID_ARG;
   csffn_status st = check_slots(T, k);
   if (st != CSFFN_OK) return st;
-  if ((st = check_width(d)) != CSFFN_OK) return st;
+  if ((st = check_width(d, xdtype == CSFFN_BF16 ? 8 : 4)) != CSFFN_OK) return st;  // rows of whole 16-byte vectors
   if (!offsets) return CSFFN_ERR_INVALID_ARG;
   if (!aligned4(offsets)) return CSFFN_ERR_ALIGNMENT;
   if (T == 0) return cuda_status(cudaMemsetAsync(offsets, 0, sizeof(int32_t) * (E + 1), as_stream(stream)));

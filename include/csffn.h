@@ -371,7 +371,8 @@ size_t csffn_moe_dispatch_workspace_size(int max_rows, int n_experts);
  *   order[p] = slot at sorted position p (int32 [T * k]); pos[s] = sorted position of slot s, or -1
  *   (int32 [T, k]); xs[p, :] = x[order[p] / k, :] ([T * k, d] in xdtype).
  *   Entries of order and rows of xs at and behind offsets[E] are left as they were.
- *   x: [T, d] in xdtype (csffn_dtype).  No output may overlap an input or another output (refused).
+ *   x: [T, d] in xdtype (csffn_dtype); d % 8 == 0 for bf16, d % 4 == 0 for fp32.  No output may
+ *   overlap an input or another output (refused).
  *   1 <= k <= CSFFN_MAX_TOPK, 1 <= E <= CSFFN_MAX_EXPERTS.
  *   T == 0: writes offsets = 0. */
 csffn_status csffn_moe_dispatch(const void* x, int xdtype, const int32_t* ids, int T, int k, int E, int d,

@@ -174,6 +174,16 @@ def test_dispatch_sizes_of_its_forms(T, k):
     assert torch.equal(got["xs"][:n], x[want[:n] // k]) and (got["xs"][n:] == 7.0).all()
 
 
+@pytest.mark.parametrize("T,d", [(5, 12), (700, 260), (9000, 20)])
+def test_dispatch_fp32_rows_of_odd_multiples_of_four(T, d):
+    g = gen(T + d)
+    x, ids = rnd(g, T, d, dtype=F32), random_ids(g, T, 6, 2, 0.1)
+    check_dispatch(x, ids, 6, run_dispatch(x, ids, 6))
+    with pytest.raises(cs.CsffnError) as e:
+        run_dispatch(x.bfloat16(), ids, 6)
+    assert e.value.status == _abi.ERR_ALIGNMENT
+
+
 def test_dispatch_one_expert_takes_all():
     x, ids = rnd(gen(1), 2000, 32), torch.full((2000, 2), 5, dtype=I32, device="cuda")
     check_dispatch(x, ids, 9, run_dispatch(x, ids, 9))

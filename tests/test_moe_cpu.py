@@ -129,6 +129,15 @@ def test_dispatch_refusals(lib):
     assert lib.csffn_moe_dispatch_workspace_size((1 << 22) + 1, 8) == lib.csffn_moe_dispatch_workspace_size(8, 513) == 0
 
 
+def test_dispatch_widths_by_type(lib):
+    """Rows are whole 16-byte vectors: multiples of 8 in bf16, of 4 in fp32 (then the workspace is refused)."""
+    def f(dt, d):
+        return lib.csffn_moe_dispatch(FAKE, dt, FAKE, 4, 2, 8, d, FAKE, FAKE, FAKE, FAKE, FAKE, 100, None)
+    assert f(_abi.F32, 260) == f(_abi.F32, 12) == f(_abi.BF16, 264) == WS
+    assert f(_abi.F32, 258) == f(_abi.BF16, 260) == ALIGN
+    assert f(_abi.F32, 4) == f(_abi.F32, 16388) == SHAPE
+
+
 def test_dispatch_refuses_overlapping_buffers(lib):
     """T = 4, k = 2, E = 8, rows of 512 bytes: every buffer at an address of its own, then one output moved
     onto another buffer, onto its last word, or to where the two share one word."""
