@@ -5,11 +5,12 @@
 // and the gate, all loaded before the first sum.  mean(y^2) is one reduction over the group, h'
 // follows in registers, mean(h'^2) is a second one, so h and y are read once and h' and xn written
 // once (against a pass per norm and one for the residual).  Bound by memory: 8192 x 4096 with a gate
-// per token 81.6 us, the copy rate (85.4 us with two chunks on half the threads); with a gate per
-// channel 73 us (84%).  Rows of 8192 on 512 threads 83 us for 4096 tokens (on 1024: 113, on 256: 98);
-// rows of 16384 leave one or two rows per SM and wait for their sums: 61%.  The next kernel is not let
-// start early (tcgen05.cuh); its CTAs would only take the place of rows: 512 rows of 2048, one call after
-// the other, 3.6 us, 4.8 with the trigger.
+// per token 81.6 us one after the other in a graph (81.9 at the measured copy rate; 85 to 90 called from
+// the host; 85.4 in a graph with two chunks on half the threads); with a gate per channel 73 us (84%).
+// Rows of 8192 on 512 threads 83 us for 4096 tokens (on 1024: 113, on 256: 98); rows of 16384 leave one
+// or two rows per SM and wait for their sums: 61%.  The next kernel is not let start early (tcgen05.cuh);
+// its CTAs would only take the place of rows: 512 rows of 2048, one call after the other, 3.6 us, 4.8
+// with the trigger.
 #include "common.cuh"
 #include "kernels.h"
 #include "tcgen05.cuh"

@@ -17,8 +17,8 @@
 // logits become NaN.
 //
 // Both kernels read the router weights after the dependency wait only, as they do x: the weights may
-// be another call's output (a router normalised per call by csffn_block_norm), and that kernel, or a
-// chained one after it, has let this one start before the weights were complete.
+// be another call's output (a router normalised per call by csffn_block_norm).  Fetching them before it
+// would gain next to nothing: 16 tokens x 128 experts 4.0 us against 4.1, 8192 tokens the same.
 #include "common.cuh"
 #include "kernels.h"
 #include "tcgen05.cuh"

@@ -11,8 +11,9 @@
 //
 // Gather: one pass over the tokens: a token's row is read once and written to the positions of its
 // slots (d bytes read + k d written, against k d + k d for a gather by position).  8192 tokens x 8 of
-// 64 experts, d 2048 bf16: the three kernels 53 us, of which the gather is 43 (41 at the copy rate);
-// 13 tokens in the one kernel: 4.5 us, the latency of its chain of loads, counts and stores.
+// 64 experts, d 2048 bf16: the three kernels 60 us with random experts (46 at the copy rate), 53 where
+// every token has the same ones and an eighth has none, of which the gather is 43 (41); 13 tokens in the
+// one kernel: 3.4 us, the latency of its chain of loads, counts and stores.
 //
 // The kernels that write rows (xs, out) do not let the next kernel start early: the rows may be weights
 // of the call that follows (tcgen05.cuh).  It costs nothing: combine, 512 tokens, call after call 4.6 us
@@ -20,7 +21,7 @@
 //
 // Combine: one pass over the tokens: each thread owns 8 columns and adds the token's k rows in slot
 // order in fp32, so the sum does not depend on timing (no atomics).  Bound by memory: the same
-// tokens 46 us (41 at the copy rate).
+// tokens 49.5 us (46 at the copy rate), with an eighth of none 45 (41).
 #include "common.cuh"
 #include "kernels.h"
 #include "tcgen05.cuh"

@@ -26,7 +26,7 @@
 // compacts idx / a_val / count.  Both are launched as programmatic dependents of the kernel before
 // them on the stream: a streaming CTA may start on an SM the previous step's streaming CTA has left
 // while the previous step still finishes, and it fetches its first W_gate rows (weights, which no
-// kernel writes) before griddepcontrol.wait; everything else -- the tokens, the candidate list, the
+// kernel that lets its successors start early writes) before griddepcontrol.wait; everything else -- the tokens, the candidate list, the
 // workspace, the outputs -- is touched only after it.
 // Every wait is bounded (a second); a wait that runs out records the timeout in the error word and
 // ends the CTA's loops, after waiting (again bounded) for the CTA's own copies still in flight.

@@ -320,7 +320,12 @@ csffn_status csffn_sparse_ffn_forward_static(const csffn_layer* layer, const voi
  * These calls take any number of tokens (decode steps and prompts).  Every count that depends on
  * the routing stays on the device, so the whole step can be captured in a CUDA graph.  All of them
  * are bit-for-bit repeatable.  Pointers, streams, errors and workspaces as above; T == 0 (or
- * rows == 0) is an empty call.
+ * rows == 0) is an empty call.  Outputs must not overlap inputs or one another except where it says so.
+ * A workspace of these calls serves these calls only: those on a csffn_layer keep state elsewhere in
+ * theirs (csffn_workspace_init makes one fit for the other).  Rows and weights are finite by
+ * contract; a value that overflows stays in its row: a v past bf16's range makes its row of ys +-inf
+ * or NaN, no other.
+ * Any input, weights and router weights too, may be the output of a call just before on the stream.
  * --------------------------------------------------------------------------------------------- */
 #define CSFFN_MAX_EXPERTS 512
 #define CSFFN_MAX_TOPK 16
